@@ -1,0 +1,103 @@
+// Launchers of the operators around the layer (rmsnorm.hip, linear_i8.hip,
+// vocab_loss.hip). All launch on `stream`; their callers have validated the
+// sizes (poetx_model.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace poetx {
+
+// The norm of x + res (res optional) with y or int8 codes q out; gain null:
+// only the row quantisation of x.
+struct NormFwdDesc {
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  const void* res = nullptr;
+  int64_t ldr = 0;
+  const float* gain = nullptr;
+  float eps = 0.f;
+  void* h = nullptr;
+  void* y = nullptr;
+  float* rstd = nullptr;
+  int8_t* q = nullptr;
+  float* scale = nullptr;
+  int64_t T = 0, n = 0;
+  bool bf16 = true;
+};
+void norm_forward(const NormFwdDesc& d, hipStream_t stream);
+
+struct NormBwdDesc {
+  const void* dy = nullptr;
+  int64_t lddy = 0;
+  const void* h = nullptr;
+  const float* rstd = nullptr;
+  const float* gain = nullptr;
+  const void* dh = nullptr;
+  int64_t lddh = 0;
+  void* dx = nullptr;
+  float* part = nullptr;   // norm_bwd_groups(T, n) * n floats of scratch, with dgain
+  float* dgain = nullptr;
+  int64_t T = 0, n = 0;
+  bool bf16 = true;
+};
+// Row groups of the backward: each sums its rows' share of dgain.
+int norm_bwd_groups(int64_t T, int64_t n);
+void norm_backward(const NormBwdDesc& d, hipStream_t stream);
+
+// z = (xq wt^T) scaled per row and column (poetx_linear_i8).
+struct LinearI8Desc {
+  const int8_t* xq = nullptr;
+  const float* xs = nullptr;
+  const int8_t* wt = nullptr;
+  const float* ws = nullptr;
+  void* z = nullptr;
+  int64_t ldz = 0;
+  int64_t T = 0, m = 0, n = 0;
+  bool out_bf16 = true;
+  int32_t* part = nullptr;  // linear_i8_part_bytes(T, m, n) bytes of scratch
+};
+size_t linear_i8_part_bytes(int64_t T, int64_t m, int64_t n);
+void linear_i8(const LinearI8Desc& d, hipStream_t stream);
+
+// Vocabulary cross entropy (poetx_vocab_loss_*). The counted tokens (target
+// in [0, V)) are gathered to the front: compact row c is token idx[c], and
+// pos[t] is token t's compact row or -1.
+struct VocabRows {
+  int32_t* pos;    // [T]
+  int32_t* idx;    // [T]
+  int32_t* tgt;    // [T] target of compact row c
+  float* g;        // [T] upstream gradient of compact row c (backward)
+  float* lse;      // [T] lse of compact row c (backward)
+  int32_t* count;  // [1] counted tokens
+};
+struct VocabDesc {
+  const void* h = nullptr;
+  int64_t ldh = 0;
+  const void* w = nullptr;
+  int64_t ldw = 0;
+  const int64_t* target = nullptr;
+  int64_t T = 0, d = 0, V = 0;
+  bool bf16 = true;
+  VocabRows rows{};
+  void* hc = nullptr;       // [T][d] compact rows of h
+  // forward
+  float2* stat = nullptr;   // [ceil(V / 256)][T] maximum and sum of a tile's columns (bf16)
+  float* tl = nullptr;      // [T] target's logit of a compact row
+  float2* run = nullptr;    // [T] running maximum and sum (f32)
+  float* loss = nullptr;
+  float* lse = nullptr;
+  // backward
+  const float* lse_in = nullptr;
+  const float* dloss = nullptr;
+  float scale = 1.f;
+  void* p = nullptr;        // [T][piece] gradient of a piece's logits (f32 forward: the logits)
+  int64_t piece = 0;        // a multiple of 256
+  float* acc = nullptr;     // [T][d] sum of dh over the pieces (more than one)
+  void* dh = nullptr;
+  void* dw = nullptr;
+};
+bool vocab_forward(const VocabDesc& d, hipStream_t stream);
+bool vocab_backward(const VocabDesc& d, hipStream_t stream);
+
+}  // namespace poetx

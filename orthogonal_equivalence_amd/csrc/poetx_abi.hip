@@ -20,6 +20,7 @@
 // writes the merged weight straight into the frame of the next permutations.
 // W0 in the original frame exists only on request (poetx_weight_export).
 #include "../../include/poetx.h"
+#include "abi_common.hpp"
 #include "common.hpp"
 #include "gemm.hpp"
 #include "kernels.hpp"
@@ -39,15 +40,6 @@ struct Side {
   int b;
   int nblk;
 };
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// every pointer non-null and 16-byte aligned
-bool ptrs_ok(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p || !aligned16(p)) return false;
-  return true;
-}
 
 // Size limits. Tokens: every token count the kernels form (T rounded up to a
 // tile, a split's share) stays an int. Blocks: the CNP launches put the
@@ -95,19 +87,6 @@ int64_t packed_len(const Side& s) {
   const int64_t last = s.dim - static_cast<int64_t>(s.nblk - 1) * s.b;
   return static_cast<int64_t>(s.nblk - 1) * (static_cast<int64_t>(s.b) * (s.b - 1) / 2) + last * (last - 1) / 2;
 }
-
-// Bump allocator over the caller's workspace (256-byte aligned pieces).
-struct Carve {
-  char* base;
-  size_t off = 0;
-  explicit Carve(void* p) : base(static_cast<char*>(p)) {}
-  template <typename T>
-  T* take(int64_t count, size_t esize = sizeof(T)) {
-    const size_t o = off;
-    off = (off + static_cast<size_t>(count) * esize + 255) & ~static_cast<size_t>(255);
-    return base ? reinterpret_cast<T*>(base + o) : nullptr;
-  }
-};
 
 // Split of a token reduction over T so that about `target` workgroups run.
 struct Split {
@@ -381,25 +360,28 @@ hipEvent_t prof_event() {
   return e;
 }
 
-struct ProfScope {
-  bool on = false;
-  hipStream_t st;
-  ProfRec rec{};
-  ProfScope(const char* name, hipStream_t s) : st(s) {
-    std::lock_guard<std::mutex> g(g_prof_mu);
-    if (!g_prof_on) return;
-    rec.name = name;
-    rec.start = prof_event();
-    rec.stop = prof_event();
-    if (!rec.start || !rec.stop) return;
-    on = hipEventRecord(rec.start, st) == hipSuccess;
-  }
-  ~ProfScope() {
-    if (!on) return;
-    std::lock_guard<std::mutex> g(g_prof_mu);
-    if (hipEventRecord(rec.stop, st) == hipSuccess) g_prof.push_back(rec);
-  }
-};
+}  // namespace
+
+namespace poetx {
+
+ProfScope::ProfScope(const char* name, hipStream_t s) : st_(s), name_(name) {
+  std::lock_guard<std::mutex> g(g_prof_mu);
+  if (!g_prof_on) return;
+  start_ = prof_event();
+  stop_ = prof_event();
+  if (!start_ || !stop_) return;
+  on_ = hipEventRecord(start_, st_) == hipSuccess;
+}
+
+ProfScope::~ProfScope() {
+  if (!on_) return;
+  std::lock_guard<std::mutex> g(g_prof_mu);
+  if (hipEventRecord(stop_, st_) == hipSuccess) g_prof.push_back(ProfRec{name_, start_, stop_});
+}
+
+}  // namespace poetx
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // building blocks
@@ -704,8 +686,10 @@ bool cnp_bwd_group(const poetx_layer* L, const Group& g, const float* q0, const 
 thread_local hipError_t g_last_hip = hipSuccess;
 thread_local std::string g_last_hip_msg;
 
-// Drops a HIP error left pending by earlier calls of other code on this
-// thread, so that launch_status() sees only this entry point's launches.
+}  // namespace
+
+namespace poetx {
+
 void clear_pending_error() { (void)hipGetLastError(); }
 
 int launch_status() {
@@ -714,6 +698,10 @@ int launch_status() {
   g_last_hip = e;
   return POETX_EHIP;
 }
+
+}  // namespace poetx
+
+namespace {
 
 int check_ws(const poetx_layer* L, int64_t T, int op, const void* ws, size_t ws_bytes) {
   const size_t need = ws_bytes_for(L, T, op);
