@@ -92,15 +92,10 @@ POETX_API size_t poetx_rmsnorm_ws_bytes(int64_t T, int64_t n);
  * m and n multiples of 16, 16 <= n <= 2^24, 16 <= m <= 131056 (the largest
  * width whose sums of any int8 codes stay below 2^31), T <= 2^24.
  *   xq [T][m] int8, x_scale [T], wt [n][m] int8, w_scale [n].
- *   z [T][n] (stride ldz), out_dtype POETX_BF16 or POETX_F32.
- *   ws: poetx_linear_i8_ws_bytes(T, m, n) bytes. */
+ *   z [T][n] (stride ldz), out_dtype POETX_BF16 or POETX_F32. */
 POETX_API int poetx_linear_i8(int64_t T, int64_t m, int64_t n, int out_dtype, const int8_t* xq,
                               const float* x_scale, const int8_t* wt, const float* w_scale, void* z, int64_t ldz,
-                              void* ws, size_t ws_bytes, hipStream_t stream);
-
-/* Workspace bytes of poetx_linear_i8; 0 for invalid sizes or where none is
- * needed. */
-POETX_API size_t poetx_linear_i8_ws_bytes(int64_t T, int64_t m, int64_t n);
+                              hipStream_t stream);
 
 /* wt [n][m] = transpose of w0 [m][n] (int8 codes, sizes as above). */
 POETX_API int poetx_linear_i8_prepare(int64_t m, int64_t n, const int8_t* w0, int8_t* wt, hipStream_t stream);

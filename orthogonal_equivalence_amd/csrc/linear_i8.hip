@@ -1,6 +1,11 @@
 // int8 product with one scale per token and output: z[t][c] = xs[t] ws[c]
 // sum_k xq[t][k] wt[c][k], exact int32 sums on v_mfma_i32_32x32x32_i8, the
 // scales in the epilogue.
+//
+// Many tokens are bound by the matrix cores and by the LDS that feeds them
+// (tile_gemm.hpp); in between, the K loop of a tile is a chain of latencies,
+// which smaller tiles spread over more CUs. Few tokens are bound by the n m
+// bytes of the weight (k_linear_i8_few).
 #include "model_kernels.hpp"
 #include "tile_gemm.hpp"
 
@@ -43,15 +48,161 @@ void launch(const I8Args& a, bool bf16, hipStream_t st) {
   else hipLaunchKernelGGL((k_linear_i8<Cfg, float>), dim3(tm * tn), dim3(Cfg::NT), 0, st, a, tm, tn);
 }
 
-}  // namespace
+template <int BM, int BN, int WM, int WN, int NS, int KG>
+void launch_tail(const I8Args& a, bool bf16, hipStream_t st) {
+  if (a.m % 128) launch<TileCfg<1, BM, BN, WM, WN, NS, true, true, true, KG>>(a, bf16, st);
+  else launch<TileCfg<1, BM, BN, WM, WN, NS, true, true, false, KG>>(a, bf16, st);
+}
 
-size_t linear_i8_part_bytes(int64_t, int64_t, int64_t) { return 0; }
+// Up to 32 TT tokens: a workgroup computes 32 OB outputs, its NW waves taking
+// 128-byte pieces of K in turn (a row's next NW pieces are read at the same
+// time). Bound by the weight's bytes, which are read once. A wave streams its pieces of weights and codes through an LDS ring of
+// its own, D pieces deep, with direct loads of whole 128-byte lines, and waits
+// for nothing but its own loads: no barrier until the waves' sums are joined.
+template <int OB, int TT, int NW, int D>
+struct FewCfg {
+  static constexpr int L = 4 * (OB + TT);           // 1 KB loads of a piece
+  static constexpr int PIECE = L * 1024;
+  static constexpr int RING = NW * D * PIECE;
+  static constexpr int SUMS = NW * TT * 32 * (32 * OB + 4) * 4;
+  static constexpr int LDS = RING > SUMS ? RING : SUMS;
+  static_assert(LDS <= 160 * 1024 && (D - 1) * L <= 63, "ring");
+};
+
+template <int OB, int TT, int NW, int D, typename O>
+__global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
+  using C = FewCfg<OB, TT, NW, D>;
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 32 * OB;
+  char* ring = smem + wave * D * C::PIECE;
+
+  TileLoader<32 * OB, 4 * OB, true, 1, true> lw;
+  TileLoader<32 * TT, 4 * TT, true, 1, true> lx;
+  lw.init(a.w, n0, 0, 0, lane);
+  lx.init(a.x, 0, 0, 0, lane);
+  const int pieces = (a.m + 127) / 128;
+  // past the last piece nothing is in range: zeros, no memory read
+  auto load = [&](int p, char* to) {
+    const int64_t kleft = a.m - static_cast<int64_t>(p) * 128;
+#pragma unroll
+    for (int i = 0; i < 4 * OB; ++i) lw.load(i, p, kleft, to, 0);
+#pragma unroll
+    for (int i = 0; i < 4 * TT; ++i) lx.load(i, p, kleft, to + 4096 * OB, 0);
+  };
+
+  i32x16_t acc[TT][OB];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int o = 0; o < OB; ++o)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[t][o][i] = 0;
+  const int r = lane & 31, half = lane >> 5;
+  const int sw = (r & 7) ^ ((r >> 3) & 1);
+
+#pragma unroll
+  for (int s = 0; s < D - 1; ++s) load(wave + s * NW, ring + s * C::PIECE);
+  int cur = 0;
+  for (int p = wave; p < pieces; p += NW) {
+    // the slot read in the last turn is free once its reads are done
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load(p + (D - 1) * NW, ring + (cur == 0 ? D - 1 : cur - 1) * C::PIECE);
+    tg_wait_vm<(D - 1) * C::L>();
+    const char* st = ring + cur * C::PIECE;
+    cur = cur == D - 1 ? 0 : cur + 1;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int off = r * 128 + (((2 * kk + half) ^ sw) << 4);
+      i32x4_t wf[OB], xf[TT];
+#pragma unroll
+      for (int o = 0; o < OB; ++o) wf[o] = *reinterpret_cast<const i32x4_t*>(st + o * 4096 + off);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xf[t] = *reinterpret_cast<const i32x4_t*>(st + (OB + t) * 4096 + off);
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int o = 0; o < OB; ++o)
+          acc[t][o] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[o], xf[t], acc[t][o], 0, 0, 0);
+    }
+  }
+  tg_wait_vm<0>();
+  __syncthreads();
+
+  // sums [wave][token][output]
+  constexpr int ROW = 32 * OB + 4;
+  int* part = reinterpret_cast<int*>(smem);
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int o = 0; o < OB; ++o)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<i32x4_t*>(part + ((wave * TT + t) * 32 + r) * ROW + o * 32 + q * 8 + half * 4) =
+            i32x4_t{acc[t][o][4 * q], acc[t][o][4 * q + 1], acc[t][o][4 * q + 2], acc[t][o][4 * q + 3]};
+  __syncthreads();
+  O* z = static_cast<O*>(a.z);
+  for (int e = threadIdx.x; e < min(a.T, 32 * TT) * 32 * OB; e += 64 * NW) {
+    const int t = e / (32 * OB), c = e % (32 * OB);
+    if (n0 + c >= a.n) continue;
+    int s = 0;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) s += part[(v * TT * 32 + t) * ROW + c];
+    store_from_f32(z + t * a.ldz + n0 + c, static_cast<float>(s) * a.xs[t] * a.ws[n0 + c]);
+  }
+}
+
+template <int OB, int TT, int NW, int D>
+void launch_few(const I8Args& a, bool bf16, hipStream_t st) {
+  const dim3 grid((a.n + 32 * OB - 1) / (32 * OB));
+  if (bf16) hipLaunchKernelGGL((k_linear_i8_few<OB, TT, NW, D, bf16_t>), grid, dim3(64 * NW), 0, st, a);
+  else hipLaunchKernelGGL((k_linear_i8_few<OB, TT, NW, D, float>), grid, dim3(64 * NW), 0, st, a);
+}
+
+}  // namespace
 
 void linear_i8(const LinearI8Desc& d, hipStream_t st) {
   const I8Args a{{d.xq, d.m, d.T, d.m}, {d.wt, d.m, d.n, d.m}, d.xs, d.ws, d.z, d.ldz,
                  static_cast<int>(d.T), static_cast<int>(d.n), static_cast<int>(d.m)};
-  if (d.m % 128) launch<TileCfg<1, 256, 256, 2, 4, true, true, true>>(a, d.out_bf16, st);
-  else launch<TileCfg<1, 256, 256, 2, 4, true, true, false>>(a, d.out_bf16, st);
+  // Few tokens: one ring a wave. 64 outputs a workgroup where 32 would make
+  // more than one round over the 256 CUs (measured at T = 1: m = 4096, n =
+  // 14336 10.4 us against 14.8; m = 13824, n = 5120 13.7 against 12.1).
+  // 33 to 64 tokens with that many outputs go to the tiles (T = 64, same
+  // shapes: 12.5 us against 20.1; 22.8 against 18.8).
+  if (a.T <= 32) {
+    if (a.n > 256 * 32) launch_few<2, 1, 4, 2>(a, d.out_bf16, st);
+    else launch_few<1, 1, 4, 4>(a, d.out_bf16, st);
+    return;
+  }
+  if (a.T <= 64 && a.n <= 256 * 32) {
+    launch_few<1, 2, 4, 3>(a, d.out_bf16, st);
+    return;
+  }
+  // The tile whose rounds over the 256 CUs cost least. A round's time (us) as
+  // measured at m = 4096 with every CU at work; it grows with m alike for all.
+  struct Tile {
+    int bm, bn;
+    double us;
+  };
+  static constexpr Tile kTiles[] = {{64, 64, 10.7}, {64, 128, 15.5}, {128, 128, 21.4}, {256, 128, 35.0}, {256, 256, 64.0}};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 5; ++i) {
+    const int64_t tiles = int64_t((a.T + kTiles[i].bm - 1) / kTiles[i].bm) * ((a.n + kTiles[i].bn - 1) / kTiles[i].bn);
+    const double us = static_cast<double>((tiles + 255) / 256) * kTiles[i].us;
+    if (i == 0 || us < least) {
+      best = i;
+      least = us;
+    }
+  }
+  switch (best) {
+    case 0: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
+    case 1: launch_tail<64, 128, 2, 2, 4, 1>(a, d.out_bf16, st); return;
+    case 2: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;
+    case 3: launch_tail<256, 128, 4, 2, 3, 1>(a, d.out_bf16, st); return;
+    default: launch_tail<256, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
+  }
 }
 
 }  // namespace poetx

@@ -223,20 +223,11 @@ bool i8_sizes_ok(int64_t m, int64_t n) {
 }
 }  // namespace
 
-size_t poetx_linear_i8_ws_bytes(int64_t T, int64_t m, int64_t n) {
-  if (!i8_sizes_ok(m, n) || T <= 0 || T > kVocabTokens) return 0;
-  return linear_i8_part_bytes(T, m, n);
-}
-
 int poetx_linear_i8(int64_t T, int64_t m, int64_t n, int out_dtype, const int8_t* xq, const float* x_scale,
-                    const int8_t* wt, const float* w_scale, void* z, int64_t ldz, void* ws, size_t ws_bytes,
-                    hipStream_t stream) {
+                    const int8_t* wt, const float* w_scale, void* z, int64_t ldz, hipStream_t stream) {
   if (!i8_sizes_ok(m, n) || T < 0 || T > kVocabTokens || !act_ok(out_dtype)) return POETX_EINVAL;
   if (!stride_ok(ldz, n, elem(out_dtype))) return POETX_EINVAL;
-  if (T > 0) {
-    if (!ptrs_ok({xq, x_scale, wt, w_scale, z})) return POETX_EINVAL;
-    if (const int e = ws_ok(ws, ws_bytes, poetx_linear_i8_ws_bytes(T, m, n))) return e;
-  }
+  if (T > 0 && !ptrs_ok({xq, x_scale, wt, w_scale, z})) return POETX_EINVAL;
   clear_pending_error();
   if (T == 0) return POETX_OK;
   LinearI8Desc d;
@@ -250,7 +241,6 @@ int poetx_linear_i8(int64_t T, int64_t m, int64_t n, int out_dtype, const int8_t
   d.m = m;
   d.n = n;
   d.out_bf16 = out_dtype == POETX_BF16;
-  d.part = static_cast<int32_t*>(ws);
   ProfScope p("linear_i8", stream);
   linear_i8(d, stream);
   return launch_status();

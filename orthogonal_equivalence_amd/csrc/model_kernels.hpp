@@ -55,9 +55,7 @@ struct LinearI8Desc {
   int64_t ldz = 0;
   int64_t T = 0, m = 0, n = 0;
   bool out_bf16 = true;
-  int32_t* part = nullptr;  // linear_i8_part_bytes(T, m, n) bytes of scratch
 };
-size_t linear_i8_part_bytes(int64_t T, int64_t m, int64_t n);
 void linear_i8(const LinearI8Desc& d, hipStream_t stream);
 
 // Vocabulary cross entropy (poetx_vocab_loss_*). The counted tokens (target

@@ -3,8 +3,8 @@
 // C per workgroup, left in registers for an epilogue of the caller's.
 //
 //  * Operands go global -> LDS with buffer loads that write LDS directly, 128
-//    bytes of K (64 bfloat16, 128 int8) a step, two stages, one barrier a
-//    step, the next stage's loads spread over the current stage's MFMAs. The
+//    bytes of K (64 bfloat16, 128 int8) a step, NS stages, one barrier a
+//    step, a later stage's loads spread over the current stage's MFMAs. The
 //    buffer's record count ends at the operand's last byte, so rows past the
 //    end read as zero without an address select; with KTAIL, 16-byte chunks
 //    past the end of K get an offset outside the buffer for the same effect
@@ -41,11 +41,14 @@ struct TileOperand {
 };
 
 // ES: element bytes. AKC / BKC: operand K-contiguous. WM x WN waves.
-template <int ES_, int BM_, int BN_, int WM_, int WN_, bool AKC_, bool BKC_, bool KTAIL_>
+// NS: stages; the loads of NS - 1 K steps are in flight. KG: groups of WM x WN
+// waves that take K steps in turn, each with stages of its own; their sums
+// are joined at the end and left with the first group.
+template <int ES_, int BM_, int BN_, int WM_, int WN_, int NS_, bool AKC_, bool BKC_, bool KTAIL_, int KG_ = 1>
 struct TileCfg {
-  static constexpr int ES = ES_, BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int ES = ES_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KG = KG_;
   static constexpr bool AKC = AKC_, BKC = BKC_, KTAIL = KTAIL_;
-  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int NW = WM * WN, NT = 64 * NW * KG;  // waves of a group, threads
   static constexpr int BK = 128 / ES;              // K of a step
   static constexpr int WTM = BM / WM, WTN = BN / WN;
   static constexpr int TM = WTM / 32, TN = WTN / 32;
@@ -53,7 +56,9 @@ struct TileCfg {
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads a wave
   static constexpr int SLAB = WTN + 8;             // epilogue slab row, floats
   static constexpr int SLABS = NW * 32 * SLAB * 4;
-  static constexpr int LDS = 2 * STAGE > SLABS ? 2 * STAGE : SLABS;
+  static constexpr int RING = NS * STAGE;
+  static constexpr int JOIN = (KG - 1) * BM * BN * 4;
+  static constexpr int LDS = KG * RING > SLABS ? (KG * RING > JOIN ? KG * RING : JOIN) : (SLABS > JOIN ? SLABS : JOIN);
   static_assert(ES == 2 || (AKC && BKC), "transposed reads are 16-bit");
   static_assert(LA >= 1 && LB >= 1 && LDS <= 160 * 1024, "tile");
 };
@@ -66,6 +71,29 @@ template <>
 struct TileAcc<1> {
   typedef i32x16_t type;
 };
+
+template <int ES>
+struct TileQuad {
+  typedef f32x4_t type;
+};
+template <>
+struct TileQuad<1> {
+  typedef i32x4_t type;
+};
+template <int ES>
+struct TileFrag {
+  typedef bf16x8_t type;
+};
+template <>
+struct TileFrag<1> {
+  typedef i32x4_t type;
+};
+__device__ __forceinline__ f32x16_t tile_mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x16_t tile_mfma(i32x4_t a, i32x4_t b, i32x16_t c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
 
 template <int N>
 __device__ __forceinline__ void tg_wait_vm() {
@@ -173,11 +201,13 @@ __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint32_t off, b
 // again for the caller when this returns (after its barrier).
 template <class Cfg>
 __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOperand& B, int m0, int n0, int64_t K,
-                                             int it0, int it1, char* smem,
+                                             int it0, int it1, char* lds,
                                              typename TileAcc<Cfg::ES>::type (&acc)[Cfg::TM][Cfg::TN]) {
   constexpr int TM = Cfg::TM, TN = Cfg::TN, LA = Cfg::LA, LB = Cfg::LB;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int gwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = gwave % Cfg::NW, group = gwave / Cfg::NW;
+  char* const smem = lds + group * Cfg::RING;
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
   const int64_t Kb = K * Cfg::ES;
 
@@ -215,19 +245,59 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
     for (int j = 0; j < TN; ++j) btr[j] = Cfg::ABYTES + tr_addr<Cfg::BN>(wn * Cfg::WTN + j * 32, lane);
   }
 
+  typedef typename TileFrag<Cfg::ES>::type Frag;
+  auto read = [&](const char* st, int kk, Frag(&fa)[TM], Frag(&fb)[TN]) {
+    const uint32_t sb = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(st));
+    if constexpr (Cfg::AKC) {
 #pragma unroll
-  for (int i = 0; i < LA; ++i) la.load(i, it0, Kb - static_cast<int64_t>(it0) * 128, smem, wave);
+      for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const Frag*>(st + abase + i * 32 * 128 + koff[kk]);
+    } else {
+      const uint32_t off = sb + kk * 16 * Cfg::BM * 2;
+      if constexpr (TM == 4) {
+        tr_read4<Cfg::BM>(atr, off, fa);
+      } else {
+        static_assert(TM == 2 || TM == 4, "fragments of a wave");
+        tr_read2<Cfg::BM>(atr[0] + off, atr[1] + off, fa[0], fa[1]);
+      }
+    }
+    if constexpr (Cfg::BKC) {
 #pragma unroll
-  for (int i = 0; i < LB; ++i) lb.load(i, it0, Kb - static_cast<int64_t>(it0) * 128, smem + Cfg::ABYTES, wave);
+      for (int j = 0; j < TN; ++j) fb[j] = *reinterpret_cast<const Frag*>(st + bbase + j * 32 * 128 + koff[kk]);
+    } else {
+      static_assert(TN == 2, "fragments of a wave");
+      const uint32_t off = sb + kk * 16 * Cfg::BN * 2;
+      tr_read2<Cfg::BN>(btr[0] + off, btr[1] + off, fb[0], fb[1]);
+    }
+  };
 
-  for (int it = it0; it < it1; ++it) {
-    tg_wait_vm<0>();
-    __syncthreads();
-    const char* st = smem + ((it - it0) & 1) * Cfg::STAGE;
-    char* nxt = smem + ((it - it0 + 1) & 1) * Cfg::STAGE;
-    // the last step loads its own slice again into the idle stage
-    const int pf = it + 1 < it1 ? it + 1 : it;
+  // steps past the last load the last slice again, into stages that are idle
+  // by then, so that the same number of loads is always in flight
+#pragma unroll
+  for (int s = 0; s < Cfg::NS - 1; ++s) {
+    const int pf = min(it0 + s * Cfg::KG + group, it1 - 1);
     const int64_t kleft = Kb - static_cast<int64_t>(pf) * 128;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) la.load(i, pf, kleft, smem + s * Cfg::STAGE, wave);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) lb.load(i, pf, kleft, smem + s * Cfg::STAGE + Cfg::ABYTES, wave);
+  }
+
+  int cur = 0;
+  for (int it = it0; it < it1; it += Cfg::KG) {
+    // this step's loads are the oldest; a bare barrier (__syncthreads would
+    // wait for the younger ones too)
+    tg_wait_vm<(Cfg::NS - 2) * (LA + LB)>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const char* st = smem + cur * Cfg::STAGE;
+    char* nxt = smem + (cur == 0 ? Cfg::NS - 1 : cur - 1) * Cfg::STAGE;
+    cur = cur == Cfg::NS - 1 ? 0 : cur + 1;
+    const int pf = min(it + (Cfg::NS - 1) * Cfg::KG + group, it1 - 1);
+    const bool mine = Cfg::KG == 1 || it + group < it1;  // a group may have no step left
+    const int64_t kleft = Kb - static_cast<int64_t>(pf) * 128;
+    Frag af[2][TM], bf[2][TN];
+    read(st, 0, af[0], bf[0]);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       constexpr int L = LA + LB;
@@ -239,51 +309,51 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
           if (i < LA) la.load(i, pf, kleft, nxt, wave);
           else lb.load(i - LA, pf, kleft, nxt + Cfg::ABYTES, wave);
         }
-      if constexpr (Cfg::ES == 2) {
-        bf16x8_t af[TM], bf[TN];
-        const uint32_t sb = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(st));
-        if constexpr (Cfg::AKC) {
+      // the next group's fragments are on their way while this group's
+      // products run
+      if (kk < 3) read(st, kk + 1, af[(kk + 1) & 1], bf[(kk + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < TM; ++i) af[i] = *reinterpret_cast<const bf16x8_t*>(st + abase + i * 32 * 128 + koff[kk]);
-        } else {
-          const uint32_t off = sb + kk * 16 * Cfg::BM * 2;
-          if constexpr (TM == 4) {
-            tr_read4<Cfg::BM>(atr, off, af);
-          } else {
-            static_assert(TM == 2 || TM == 4, "fragments of a wave");
-            tr_read2<Cfg::BM>(atr[0] + off, atr[1] + off, af[0], af[1]);
-          }
-        }
-        if constexpr (Cfg::BKC) {
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const bf16x8_t*>(st + bbase + j * 32 * 128 + koff[kk]);
-        } else {
-          static_assert(TN == 2, "fragments of a wave");
-          const uint32_t off = sb + kk * 16 * Cfg::BN * 2;
-          tr_read2<Cfg::BN>(btr[0] + off, btr[1] + off, bf[0], bf[1]);
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
-      } else {
-        i32x4_t af[TM], bf[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) af[i] = *reinterpret_cast<const i32x4_t*>(st + abase + i * 32 * 128 + koff[kk]);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) bf[j] = *reinterpret_cast<const i32x4_t*>(st + bbase + j * 32 * 128 + koff[kk]);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
-      }
+        for (int j = 0; j < TN; ++j)
+          if (mine) acc[i][j] = tile_mfma(bf[kk & 1][j], af[kk & 1][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // the re-load must land before the caller uses the LDS
+  // the last loads must land before the caller uses the LDS
   tg_wait_vm<0>();
   __syncthreads();
+  if constexpr (Cfg::KG > 1) {
+    // [group - 1][wave][tile][quad of registers][lane], 16 bytes a lane
+    typedef typename TileQuad<Cfg::ES>::type Quad;
+    Quad* const join = reinterpret_cast<Quad*>(lds) + wave * TM * TN * 256 + lane;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (group > 0)
+            join[(group - 1) * Cfg::NW * TM * TN * 256 + (i * TN + j) * 256 + q * 64] =
+                Quad{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < Cfg::KG; ++g)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const Quad v = join[(g - 1) * Cfg::NW * TM * TN * 256 + (i * TN + j) * 256 + q * 64];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+            }
+    }
+    __syncthreads();
+  }
 }
 
 // Row and column (of the workgroup's tile) of register r of tile (i, j) of a lane
@@ -303,6 +373,7 @@ template <class Cfg, class Out>
 __device__ __forceinline__ void tile_rows(const typename TileAcc<Cfg::ES>::type (&acc)[Cfg::TM][Cfg::TN], char* smem,
                                           Out&& out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave >= Cfg::NW) return;  // the first group holds the sums
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
   float* slab = reinterpret_cast<float*>(smem) + wave * 32 * Cfg::SLAB;
   constexpr int CPR = Cfg::WTN / 8, CPL = 32 * CPR / 64;

@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(256) k_vocab_scatter_f32(const float4* acc, Vo
 }
 
 template <bool KTAIL>
-using CfgLogits = TileCfg<2, 256, 256, 2, 4, true, true, KTAIL>;
-using CfgDh = TileCfg<2, 256, 256, 2, 4, true, false, false>;
-using CfgDw = TileCfg<2, 256, 256, 2, 4, false, false, false>;
+using CfgLogits = TileCfg<2, 256, 256, 2, 4, 2, true, true, KTAIL>;
+using CfgDh = TileCfg<2, 256, 256, 2, 4, 2, true, false, false>;
+using CfgDw = TileCfg<2, 256, 256, 2, 4, 2, false, false, false>;
 
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 

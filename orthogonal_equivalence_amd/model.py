@@ -11,6 +11,8 @@ rows start on 16-byte boundaries; gradients that come in broadcast (expanded)
 are copied out first.
 """
 
+import functools
+
 import torch
 
 from . import model_ops as mo
@@ -40,11 +42,10 @@ def _flat(name, t, shape, dtype, device):
 
 def _first(name, t):
     """Checks the tensor that sets an operator's shape, type and device."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name}: a two-dimensional device tensor is needed, got {tuple(t.shape)} on {t.device}")
     d = _DTYPE.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{name}: {t.dtype}, expected float32 or bfloat16")
+    if d is None or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: a two-dimensional float32 or bfloat16 device tensor is needed, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.shape, t.device, d
 
 
@@ -53,12 +54,35 @@ def _grad(t):
     return t.contiguous() if 0 in t.stride() or t.stride(-1) != 1 else t
 
 
-def _stream(device):
-    """torch's current stream of the device, as a handle. Calls on another
-    device than the current one run under its guard."""
-    return torch.cuda.current_stream(device).cuda_stream
+def _on_device(f):
+    """Runs f with its first tensor's device current, as its allocations and
+    the library's launches need."""
+    @functools.wraps(f)
+    def g(t, *args, **kw):
+        if t.is_cuda and t.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return f(t, *args, **kw)
+        return f(t, *args, **kw)
+    return g
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """The entry point on torch's current stream (its raw handle: a call's
+    host time is a few microseconds, and a Stream object would cost two)."""
+    st = getattr(mo._lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != px.POETX_OK:
+        raise px.PoetxError(name, st)
+
+
+def _scratch(need, dev):
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+@_on_device
 def rms_norm(x, gain, residual=None, eps=1e-6):
     """(h, y, rstd): h = x + residual in x's type (x itself without one), y =
     h / sqrt(mean(h^2) + eps) * gain, computed before h is rounded, and the
@@ -67,14 +91,15 @@ def rms_norm(x, gain, residual=None, eps=1e-6):
     ldx = _rows("x", x, x.shape, x.dtype, dev)
     ldr = _rows("residual", residual, x.shape, x.dtype, dev) if residual is not None else 0
     _flat("gain", gain, (n,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        h = torch.empty((T, n), dtype=x.dtype, device=dev) if residual is not None else None
-        y = torch.empty((T, n), dtype=x.dtype, device=dev)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-        mo.poetx_rmsnorm_forward(T, n, dt, x, ldx, residual, ldr, gain, eps, h, y, rstd, _stream(dev))
+    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    _call("poetx_rmsnorm_forward", dev, T, n, dt, x.data_ptr(), ldx, _ptr(residual), ldr, gain.data_ptr(), eps, _ptr(h),
+          y.data_ptr(), rstd.data_ptr())
     return (h if h is not None else x), y, rstd
 
 
+@_on_device
 def rms_norm_q8(x, gain, residual=None, eps=1e-6):
     """(h, q, scale): the norm's rows as int8 codes with one scale a token,
     the input of ``linear_i8``."""
@@ -82,25 +107,26 @@ def rms_norm_q8(x, gain, residual=None, eps=1e-6):
     ldx = _rows("x", x, x.shape, x.dtype, dev)
     ldr = _rows("residual", residual, x.shape, x.dtype, dev) if residual is not None else 0
     _flat("gain", gain, (n,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        h = torch.empty((T, n), dtype=x.dtype, device=dev) if residual is not None else None
-        q = torch.empty((T, n), dtype=torch.int8, device=dev)
-        scale = torch.empty(T, dtype=torch.float32, device=dev)
-        mo.poetx_rmsnorm_forward_q8(T, n, dt, x, ldx, residual, ldr, gain, eps, h, q, scale, _stream(dev))
+    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
+    q = torch.empty((T, n), dtype=torch.int8, device=dev)
+    scale = torch.empty(T, dtype=torch.float32, device=dev)
+    _call("poetx_rmsnorm_forward_q8", dev, T, n, dt, x.data_ptr(), ldx, _ptr(residual), ldr, gain.data_ptr(), eps,
+          _ptr(h), q.data_ptr(), scale.data_ptr())
     return (h if h is not None else x), q, scale
 
 
+@_on_device
 def quantize_rows(x):
     """(q, scale): int8 codes of x's rows with one scale a token."""
     (T, n), dev, dt = _first("x", x)
     ldx = _rows("x", x, x.shape, x.dtype, dev)
-    with torch.cuda.device(dev):
-        q = torch.empty((T, n), dtype=torch.int8, device=dev)
-        scale = torch.empty(T, dtype=torch.float32, device=dev)
-        mo.poetx_quantize_rows(T, n, dt, x, ldx, q, scale, _stream(dev))
+    q = torch.empty((T, n), dtype=torch.int8, device=dev)
+    scale = torch.empty(T, dtype=torch.float32, device=dev)
+    _call("poetx_quantize_rows", dev, T, n, dt, x.data_ptr(), ldx, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
+@_on_device
 def rms_norm_backward(dy, h, rstd, gain, dh=None):
     """(dx, dgain) from dy = dL/dy and, along the residual stream, dh = dL/dh
     past the norm; dx is the gradient of x and of the residual alike."""
@@ -114,14 +140,16 @@ def rms_norm_backward(dy, h, rstd, gain, dh=None):
     if dh is not None:
         dh = _grad(dh)
         lddh = _rows("dh", dh, dy.shape, dy.dtype, dev)
-    with torch.cuda.device(dev):
-        dx = torch.empty((T, n), dtype=dy.dtype, device=dev)
-        dgain = torch.empty(n, dtype=torch.float32, device=dev)
-        ws = torch.empty(mo.poetx_rmsnorm_ws_bytes(T, n), dtype=torch.uint8, device=dev)
-        mo.poetx_rmsnorm_backward(T, n, dt, dy, lddy, h, rstd, gain, dh, lddh, dx, dgain, ws, None, _stream(dev))
+    dx = torch.empty((T, n), dtype=dy.dtype, device=dev)
+    dgain = torch.empty(n, dtype=torch.float32, device=dev)
+    need = mo.poetx_rmsnorm_ws_bytes(T, n)
+    ws = _scratch(need, dev)
+    _call("poetx_rmsnorm_backward", dev, T, n, dt, dy.data_ptr(), lddy, h.data_ptr(), rstd.data_ptr(), gain.data_ptr(),
+          _ptr(dh), lddh, dx.data_ptr(), dgain.data_ptr(), _ptr(ws), need)
     return dx, dgain
 
 
+@_on_device
 def linear_i8_weight(w0):
     """wt [n][m] for ``linear_i8`` from int8 codes W0 [m][n], as
     ``DeviceLayer.export_w0`` returns them."""
@@ -129,12 +157,12 @@ def linear_i8_weight(w0):
         raise ValueError(f"w0: a two-dimensional device tensor is needed, got {tuple(w0.shape)} on {w0.device}")
     _flat("w0", w0, w0.shape, torch.int8, w0.device)
     m, n = w0.shape
-    with torch.cuda.device(w0.device):
-        wt = torch.empty((n, m), dtype=torch.int8, device=w0.device)
-        mo.poetx_linear_i8_prepare(m, n, w0, wt, _stream(w0.device))
+    wt = torch.empty((n, m), dtype=torch.int8, device=w0.device)
+    _call("poetx_linear_i8_prepare", w0.device, m, n, w0.data_ptr(), wt.data_ptr())
     return wt
 
 
+@_on_device
 def linear_i8(xq, x_scale, wt, w_scale, out_dtype=torch.bfloat16, out=None):
     """z[t][c] = x_scale[t] w_scale[c] sum_k xq[t][k] wt[c][k]. ``out``: a
     [T][n] tensor (rows of any stride) to write to."""
@@ -146,17 +174,15 @@ def linear_i8(xq, x_scale, wt, w_scale, out_dtype=torch.bfloat16, out=None):
     _flat("x_scale", x_scale, (T,), torch.float32, dev)
     _flat("wt", wt, (n, m), torch.int8, dev)
     _flat("w_scale", w_scale, (n,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out, ldz = torch.empty((T, n), dtype=out_dtype, device=dev), n
-        else:
-            ldz = _rows("out", out, (T, n), out.dtype, dev)
-        dt = _DTYPE.get(out.dtype)
-        if dt is None:
-            raise ValueError(f"out: {out.dtype}, expected float32 or bfloat16")
-        need = mo.poetx_linear_i8_ws_bytes(T, m, n)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        mo.poetx_linear_i8(T, m, n, dt, xq, x_scale, wt, w_scale, out, ldz, ws, None, _stream(dev))
+    if out is None:
+        out, ldz = torch.empty((T, n), dtype=out_dtype, device=dev), n
+    else:
+        ldz = _rows("out", out, (T, n), out.dtype, dev)
+    dt = _DTYPE.get(out.dtype)
+    if dt is None:
+        raise ValueError(f"out: {out.dtype}, expected float32 or bfloat16")
+    _call("poetx_linear_i8", dev, T, m, n, dt, xq.data_ptr(), x_scale.data_ptr(), wt.data_ptr(), w_scale.data_ptr(),
+          out.data_ptr(), ldz)
     return out
 
 
@@ -171,19 +197,22 @@ def _vocab(h, w, target, piece):
     return T, d, V, ldh, ldw, dev, mo.make_vocab(d, V, _NAME[h.dtype], piece)
 
 
+@_on_device
 def vocab_loss(h, w, target, piece=0):
     """(loss, lse) [T] of the softmax cross entropy of logits h w^T against
     target (int64; a target outside [0, V) is not counted: loss 0). The
     logits are not kept."""
     T, d, V, ldh, ldw, dev, D = _vocab(h, w, target, piece)
-    with torch.cuda.device(dev):
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        ws = torch.empty(mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_FORWARD), dtype=torch.uint8, device=dev)
-        mo.poetx_vocab_loss_forward(D, T, h, ldh, w, ldw, target, loss, lse, ws, None, _stream(dev))
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    need = mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_FORWARD)
+    ws = _scratch(need, dev)
+    _call("poetx_vocab_loss_forward", dev, D, T, h.data_ptr(), ldh, w.data_ptr(), ldw, target.data_ptr(),
+          loss.data_ptr(), lse.data_ptr(), _ptr(ws), need)
     return loss, lse
 
 
+@_on_device
 def vocab_loss_backward(h, w, target, lse, dloss=None, scale=1.0, piece=0):
     """(dh, dw) for the loss gradients scale * dloss [T] or, without dloss,
     for scale times the mean loss over the counted tokens. ``piece``:
@@ -193,9 +222,10 @@ def vocab_loss_backward(h, w, target, lse, dloss=None, scale=1.0, piece=0):
     if dloss is not None:
         dloss = _grad(dloss)
         _flat("dloss", dloss, (T,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        dh = torch.empty((T, d), dtype=h.dtype, device=dev)
-        dw = torch.empty((V, d), dtype=h.dtype, device=dev)
-        ws = torch.empty(mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_BACKWARD), dtype=torch.uint8, device=dev)
-        mo.poetx_vocab_loss_backward(D, T, h, ldh, w, ldw, target, lse, dloss, scale, dh, dw, ws, None, _stream(dev))
+    dh = torch.empty((T, d), dtype=h.dtype, device=dev)
+    dw = torch.empty((V, d), dtype=h.dtype, device=dev)
+    need = mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_BACKWARD)
+    ws = _scratch(need, dev)
+    _call("poetx_vocab_loss_backward", dev, D, T, h.data_ptr(), ldh, w.data_ptr(), ldw, target.data_ptr(),
+          lse.data_ptr(), _ptr(dloss), scale, dh.data_ptr(), dw.data_ptr(), _ptr(ws), need)
     return dh, dw

@@ -15,7 +15,7 @@ from .poetx import _I64, _P, _SZ, _call, _lib, _ptr, _size, _stream
 POETX_OP_VOCAB_FORWARD, POETX_OP_VOCAB_BACKWARD = 0, 1
 
 EXPORTED = [
-    "poetx_linear_i8", "poetx_linear_i8_prepare", "poetx_linear_i8_ws_bytes", "poetx_quantize_rows",
+    "poetx_linear_i8", "poetx_linear_i8_prepare", "poetx_quantize_rows",
     "poetx_rmsnorm_backward", "poetx_rmsnorm_forward", "poetx_rmsnorm_forward_q8", "poetx_rmsnorm_ws_bytes",
     "poetx_vocab_loss_backward", "poetx_vocab_loss_forward", "poetx_vocab_ws_bytes",
 ]
@@ -39,8 +39,7 @@ _sig = {
     "poetx_quantize_rows": (_INT, [_I64, _I64, _INT, _P, _I64, _P, _P, _P]),
     "poetx_rmsnorm_backward": (_INT, [_I64, _I64, _INT, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]),
     "poetx_rmsnorm_ws_bytes": (_SZ, [_I64, _I64]),
-    "poetx_linear_i8": (_INT, [_I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P]),
-    "poetx_linear_i8_ws_bytes": (_SZ, [_I64, _I64, _I64]),
+    "poetx_linear_i8": (_INT, [_I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _I64, _P]),
     "poetx_linear_i8_prepare": (_INT, [_I64, _I64, _P, _P, _P]),
     "poetx_vocab_ws_bytes": (_SZ, [_D, _I64, _INT]),
     "poetx_vocab_loss_forward": (_INT, [_D, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
@@ -76,13 +75,9 @@ def poetx_rmsnorm_ws_bytes(T, n):
     return _lib.poetx_rmsnorm_ws_bytes(T, n)
 
 
-def poetx_linear_i8(T, m, n, out_dtype, xq, x_scale, wt, w_scale, z, ldz, ws=None, ws_bytes=None, stream=None):
+def poetx_linear_i8(T, m, n, out_dtype, xq, x_scale, wt, w_scale, z, ldz, stream=None):
     _call("poetx_linear_i8", T, m, n, out_dtype, _ptr(xq), _ptr(x_scale), _ptr(wt), _ptr(w_scale), _ptr(z), ldz,
-          _ptr(ws), _size(ws, ws_bytes), _stream(stream))
-
-
-def poetx_linear_i8_ws_bytes(T, m, n):
-    return _lib.poetx_linear_i8_ws_bytes(T, m, n)
+          _stream(stream))
 
 
 def poetx_linear_i8_prepare(m, n, w0, wt, stream=None):

@@ -83,7 +83,7 @@ def test_norm_workspace_holds_a_row_per_group():
     assert 0 < big <= 1024 * 4096 * 4 and mo.poetx_rmsnorm_ws_bytes(1 << 20, 4096) == big
 
 
-LIN = dict(T=4, m=64, n=32, out=BF, xq=FAKE, xs=FAKE, wt=FAKE, ws_=FAKE, z=FAKE, ldz=32, ws=FAKE, ws_bytes=1 << 40)
+LIN = dict(T=4, m=64, n=32, out=BF, xq=FAKE, xs=FAKE, wt=FAKE, ws_=FAKE, z=FAKE, ldz=32)
 
 
 @pytest.mark.parametrize("bad", [
@@ -94,8 +94,6 @@ LIN = dict(T=4, m=64, n=32, out=BF, xq=FAKE, xs=FAKE, wt=FAKE, ws_=FAKE, z=FAKE,
 def test_linear_i8_refuses(bad):
     a = {**LIN, **bad}
     assert _status(lambda: mo.poetx_linear_i8(*a.values(), stream=0)) == px.POETX_EINVAL
-    if {"m", "n", "T"} & set(bad):
-        assert mo.poetx_linear_i8_ws_bytes(a["T"], a["m"], a["n"]) == 0
 
 
 def test_linear_i8_width_limit_keeps_every_sum_in_31_bits():
