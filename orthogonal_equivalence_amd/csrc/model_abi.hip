@@ -97,16 +97,11 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.hc = c.take<char>(T * D->d * es);
   if (bwd) {
     v.p = c.take<char>(T * v.piece * es);
-    if (!bf || v.piece < D->V) v.acc = c.take<float>(T * D->d);
+    if (v.piece < D->V) v.acc = c.take<float>(T * D->d);
     return;
   }
   v.tl = c.take<float>(T);
-  if (bf) {
-    v.stat = c.take<float2>((D->V + 255) / 256 * T);
-  } else {
-    v.run = c.take<float2>(T);
-    v.p = c.take<char>(T * v.piece * es);
-  }
+  v.stat = c.take<float2>(vocab_stat_tiles(std::max<int64_t>(T, 1), D->V, bf) * T);
 }
 
 int vocab_common(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t ldh, const void* w, int64_t ldw,
@@ -286,7 +281,7 @@ int poetx_vocab_loss_forward(const poetx_vocab* D, int64_t T, const void* h, int
   v.loss = loss;
   v.lse = lse;
   ProfScope p("vocab_loss_fwd", stream);
-  if (!vocab_forward(v, stream)) return POETX_EUNSUPPORTED;
+  vocab_forward(v, stream);
   return launch_status();
 }
 
@@ -316,7 +311,7 @@ int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const void* h, in
   v.dh = dh;
   v.dw = dw;
   ProfScope p("vocab_loss_bwd", stream);
-  if (!vocab_backward(v, stream)) return POETX_EUNSUPPORTED;
+  vocab_backward(v, stream);
   return launch_status();
 }
 

@@ -80,22 +80,23 @@ struct VocabDesc {
   VocabRows rows{};
   void* hc = nullptr;       // [T][d] compact rows of h
   // forward
-  float2* stat = nullptr;   // [ceil(V / 256)][T] maximum and sum of a tile's columns (bf16)
+  float2* stat = nullptr;   // [vocab_stat_tiles][T] maximum and sum of a tile's columns
   float* tl = nullptr;      // [T] target's logit of a compact row
-  float2* run = nullptr;    // [T] running maximum and sum (f32)
   float* loss = nullptr;
   float* lse = nullptr;
   // backward
   const float* lse_in = nullptr;
   const float* dloss = nullptr;
   float scale = 1.f;
-  void* p = nullptr;        // [T][piece] gradient of a piece's logits (f32 forward: the logits)
+  void* p = nullptr;        // [T][piece] gradient of a piece's logits
   int64_t piece = 0;        // a multiple of 256
   float* acc = nullptr;     // [T][d] sum of dh over the pieces (more than one)
   void* dh = nullptr;
   void* dw = nullptr;
 };
-bool vocab_forward(const VocabDesc& d, hipStream_t stream);
-bool vocab_backward(const VocabDesc& d, hipStream_t stream);
+// Column tiles of the forward.
+int vocab_stat_tiles(int64_t T, int64_t V, bool bf16);
+void vocab_forward(const VocabDesc& d, hipStream_t stream);
+void vocab_backward(const VocabDesc& d, hipStream_t stream);
 
 }  // namespace poetx

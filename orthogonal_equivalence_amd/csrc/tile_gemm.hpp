@@ -1,9 +1,9 @@
 // Tile engine of the operators around the layer: C[M][N] = sum_k A[m][k]
-// B[n][k] in bfloat16 (float32 sums) or int8 (int32 sums), one BM x BN tile of
-// C per workgroup, left in registers for an epilogue of the caller's.
+// B[n][k] in bfloat16 or float (float32 sums) or int8 (int32 sums), one BM x BN
+// tile of C per workgroup, left in registers for an epilogue of the caller's.
 //
 //  * Operands go global -> LDS with buffer loads that write LDS directly, 128
-//    bytes of K (64 bfloat16, 128 int8) a step, NS stages, one barrier a
+//    bytes of K (64 bfloat16, 32 float, 128 int8) a step, NS stages, one barrier a
 //    step, a later stage's loads spread over the current stage's MFMAs. The
 //    buffer's record count ends at the operand's last byte, so rows past the
 //    end read as zero without an address select; with KTAIL, 16-byte chunks
@@ -12,11 +12,13 @@
 //  * LDS rows of a K-contiguous operand are 128 bytes, chunk c of row r in
 //    slot c ^ (r & 7) ^ ((r >> 3) & 1): the 32 rows of a fragment read fall on
 //    all banks evenly.
-//  * An operand stored with K as its rows (A[k][m], B[k][n]; bfloat16) lies in
-//    LDS as it does in memory and is read with ds_read_b64_tr_b16, which hands
-//    every lane four consecutive k of its own column. Chunk c of row r is in
-//    slot c ^ 4 (r & 3), so the four rows of a read fall in four different
-//    64-byte quarters of the banks.
+//  * An operand stored with K as its rows (A[k][m], B[k][n]) lies in LDS as it
+//    does in memory. bfloat16 is read with ds_read_b64_tr_b16, which hands
+//    every lane four consecutive k of its own column; chunk c of row r is in
+//    slot c ^ 4 (r & 3) (row_swizzle), so the four rows of a read fall in four
+//    different 64-byte quarters of the banks. float is read word by word, the two halves
+//    of a wave four rows apart; slot c ^ 8 ((r >> 2) & 1) keeps their banks
+//    apart.
 //  * The MFMA takes B's fragment first: a lane then holds, for one row m
 //    (lane % 32), groups of four consecutive columns n, and a row's reduction
 //    over columns stays within a lane and its partner lane ^ 32.
@@ -59,7 +61,8 @@ struct TileCfg {
   static constexpr int RING = NS * STAGE;
   static constexpr int JOIN = (KG - 1) * BM * BN * 4;
   static constexpr int LDS = KG * RING > SLABS ? (KG * RING > JOIN ? KG * RING : JOIN) : (SLABS > JOIN ? SLABS : JOIN);
-  static_assert(ES == 2 || (AKC && BKC), "transposed reads are 16-bit");
+  static_assert((AKC || BM * ES >= 128) && (BKC || BN * ES >= 128), "rows of K of whole bank quarters");
+  static_assert(ES != 1 || (AKC && BKC), "no transposed reads of bytes");
   static_assert(LA >= 1 && LB >= 1 && LDS <= 160 * 1024, "tile");
 };
 
@@ -88,6 +91,16 @@ template <>
 struct TileFrag<1> {
   typedef i32x4_t type;
 };
+template <>
+struct TileFrag<4> {
+  typedef f32x4_t type;
+};
+// eight k of a float fragment: four products of two
+__device__ __forceinline__ f32x16_t tile_mfma(f32x4_t a, f32x4_t b, f32x16_t c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
 __device__ __forceinline__ f32x16_t tile_mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -98,6 +111,16 @@ __device__ __forceinline__ i32x16_t tile_mfma(i32x4_t a, i32x4_t b, i32x16_t c) 
 template <int N>
 __device__ __forceinline__ void tg_wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Slot of chunk c in row r of K of a tile of BT columns: c ^ row_swizzle(r),
+// the same for rows 4 (bfloat16) or 8 (float) further on. Rows of 128 bytes
+// come two to a 256-byte bank window, wider ones one or less.
+template <int BT, int ES>
+__device__ __forceinline__ int row_swizzle(int r) {
+  if constexpr (ES == 4) return ((r >> 2) & 1) << 3;
+  else if constexpr (BT * ES == 128) return ((r >> 1) & 1) << 2;
+  else return (r & 3) << 2;
 }
 
 // The loads of one operand tile: per-lane byte offsets from the tile's first
@@ -124,14 +147,14 @@ struct TileLoader {
         if constexpr (KTAIL) kchunk[i] = c * 16;
       }
     } else {
-      constexpr int RB = BT * 2, CH = RB / 16, RPI = 64 / CH;
+      constexpr int RB = BT * ES, CH = RB / 16, RPI = 64 / CH;
       base = static_cast<const char*>(o.p) + k0 * ldb + static_cast<int64_t>(row0) * ES;
       left = (o.rows - 1 - k0) * ldb + (o.cols - row0) * ES;
-      kstep = 64 * ldb;
+      kstep = 128 / ES * ldb;
 #pragma unroll
       for (int i = 0; i < L; ++i) {
         const int r = (wave * L + i) * RPI + lane / CH;
-        const int c = (lane % CH) ^ ((r & 3) << 2);
+        const int c = (lane % CH) ^ row_swizzle<BT, ES>(r);
         voff[i] = static_cast<uint32_t>(r * ldb) + c * 16;
       }
     }
@@ -158,13 +181,27 @@ __device__ __forceinline__ uint32_t tr_addr(int col0, int lane) {
   const int grp = lane >> 4, li = lane & 15;
   const int r = 8 * (grp >> 1) + (li >> 2);
   const int col = col0 + 16 * (grp & 1) + 4 * (li & 3);
-  return static_cast<uint32_t>(r * BT * 2 + (((col >> 3) ^ ((r & 3) << 2)) << 4) + (col & 7) * 2);
+  return static_cast<uint32_t>(r * BT * 2 + (((col >> 3) ^ row_swizzle<BT, 2>(r)) << 4) + (col & 7) * 2);
 }
 
-// Four / two fragments by transposed reads; each asm block waits for its own
-// results (as builtins the reads would wait for the direct loads in flight).
+// One, two or four bfloat16 fragments by transposed reads; each asm block
+// waits for its own results (as builtins the reads would wait for the direct
+// loads in flight).
 template <int BT>
-__device__ __forceinline__ void tr_read2(uint32_t a0, uint32_t a1, bf16x8_t& f0, bf16x8_t& f1) {
+__device__ __forceinline__ void tr_read(const uint32_t (&a)[1], uint32_t off, bf16x8_t (&f)[1]) {
+  typedef unsigned long long u64;
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  u64 r[2];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %2\n ds_read_b64_tr_b16 %1, %2 offset:%3\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1])
+      : "v"(a[0] + off), "n"(4 * BT * 2)
+      : "memory");
+  f[0] = __builtin_bit_cast(bf16x8_t, u64x2{r[0], r[1]});
+}
+template <int BT>
+__device__ __forceinline__ void tr_read(const uint32_t (&a)[2], uint32_t off, bf16x8_t (&f)[2]) {
   typedef unsigned long long u64;
   typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
   u64 r[4];
@@ -173,13 +210,13 @@ __device__ __forceinline__ void tr_read2(uint32_t a0, uint32_t a1, bf16x8_t& f0,
       "ds_read_b64_tr_b16 %2, %5\n ds_read_b64_tr_b16 %3, %5 offset:%6\n"
       "s_waitcnt lgkmcnt(0)"
       : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
-      : "v"(a0), "v"(a1), "n"(4 * BT * 2)
+      : "v"(a[0] + off), "v"(a[1] + off), "n"(4 * BT * 2)
       : "memory");
-  f0 = __builtin_bit_cast(bf16x8_t, u64x2{r[0], r[1]});
-  f1 = __builtin_bit_cast(bf16x8_t, u64x2{r[2], r[3]});
+  f[0] = __builtin_bit_cast(bf16x8_t, u64x2{r[0], r[1]});
+  f[1] = __builtin_bit_cast(bf16x8_t, u64x2{r[2], r[3]});
 }
 template <int BT>
-__device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint32_t off, bf16x8_t (&f)[4]) {
+__device__ __forceinline__ void tr_read(const uint32_t (&a)[4], uint32_t off, bf16x8_t (&f)[4]) {
   typedef unsigned long long u64;
   typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
   u64 r[8];
@@ -194,6 +231,22 @@ __device__ __forceinline__ void tr_read4(const uint32_t (&a)[4], uint32_t off, b
       : "memory");
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = __builtin_bit_cast(bf16x8_t, u64x2{r[2 * i], r[2 * i + 1]});
+}
+
+// Address of a lane's column in the fragment of float rows at column col0:
+// rows 8 kk + 4 (lane / 32) + e, e = 0..3, of K group kk. The rows' slots are
+// those of row 4 (lane / 32) in every group.
+template <int BT>
+__device__ __forceinline__ uint32_t row_addr_f32(int col0, int lane) {
+  const int half = lane >> 5, col = col0 + (lane & 31);
+  return static_cast<uint32_t>(half * 4 * BT * 4 + (((col >> 2) ^ row_swizzle<BT, 4>(half * 4)) << 4) + (col & 3) * 4);
+}
+template <int BT, int N>
+__device__ __forceinline__ void row_read(const char* tile, const uint32_t (&a)[N], int kk, f32x4_t (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[i][e] = *reinterpret_cast<const float*>(tile + a[i] + (kk * 8 + e) * BT * 4);
 }
 
 // The wave's TM x TN tiles of 32 x 32 of the workgroup's tile at (m0, n0),
@@ -235,14 +288,20 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) koff[kk] = lrow * 128 + (((2 * kk + (lane >> 5)) ^ sw) << 4);
   const int abase = wm * Cfg::WTM * 128, bbase = Cfg::ABYTES + wn * Cfg::WTN * 128;
-  uint32_t atr[Cfg::AKC ? 1 : TM], btr[Cfg::BKC ? 1 : TN];
+  uint32_t acol[Cfg::AKC ? 1 : TM], bcol[Cfg::BKC ? 1 : TN];
   if constexpr (!Cfg::AKC) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) atr[i] = tr_addr<Cfg::BM>(wm * Cfg::WTM + i * 32, lane);
+    for (int i = 0; i < TM; ++i) {
+      const int col = wm * Cfg::WTM + i * 32;
+      acol[i] = Cfg::ES == 2 ? tr_addr<Cfg::BM>(col, lane) : row_addr_f32<Cfg::BM>(col, lane);
+    }
   }
   if constexpr (!Cfg::BKC) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) btr[j] = Cfg::ABYTES + tr_addr<Cfg::BN>(wn * Cfg::WTN + j * 32, lane);
+    for (int j = 0; j < TN; ++j) {
+      const int col = wn * Cfg::WTN + j * 32;
+      bcol[j] = Cfg::ABYTES + (Cfg::ES == 2 ? tr_addr<Cfg::BN>(col, lane) : row_addr_f32<Cfg::BN>(col, lane));
+    }
   }
 
   typedef typename TileFrag<Cfg::ES>::type Frag;
@@ -251,22 +310,18 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
     if constexpr (Cfg::AKC) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const Frag*>(st + abase + i * 32 * 128 + koff[kk]);
+    } else if constexpr (Cfg::ES == 2) {
+      tr_read<Cfg::BM>(acol, sb + kk * 16 * Cfg::BM * 2, fa);
     } else {
-      const uint32_t off = sb + kk * 16 * Cfg::BM * 2;
-      if constexpr (TM == 4) {
-        tr_read4<Cfg::BM>(atr, off, fa);
-      } else {
-        static_assert(TM == 2 || TM == 4, "fragments of a wave");
-        tr_read2<Cfg::BM>(atr[0] + off, atr[1] + off, fa[0], fa[1]);
-      }
+      row_read<Cfg::BM, TM>(st, acol, kk, fa);
     }
     if constexpr (Cfg::BKC) {
 #pragma unroll
       for (int j = 0; j < TN; ++j) fb[j] = *reinterpret_cast<const Frag*>(st + bbase + j * 32 * 128 + koff[kk]);
+    } else if constexpr (Cfg::ES == 2) {
+      tr_read<Cfg::BN>(bcol, sb + kk * 16 * Cfg::BN * 2, fb);
     } else {
-      static_assert(TN == 2, "fragments of a wave");
-      const uint32_t off = sb + kk * 16 * Cfg::BN * 2;
-      tr_read2<Cfg::BN>(btr[0] + off, btr[1] + off, fb[0], fb[1]);
+      row_read<Cfg::BN, TN>(st, bcol, kk, fb);
     }
   };
 

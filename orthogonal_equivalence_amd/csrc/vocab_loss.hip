@@ -11,7 +11,6 @@
 // Both first gather the counted tokens (target in [0, V)) to the front, so
 // that the products spend nothing on the others and never see their rows;
 // how many there are stays on the device, and tiles past it end at once.
-#include "gemm.hpp"
 #include "model_kernels.hpp"
 #include "tile_gemm.hpp"
 
@@ -29,72 +28,84 @@ struct RowsArgs {
   const float* lse_in;  // backward (else null)
   const float* dloss;
   float scale;
+  const uint4* h;  // rows in 16-byte chunks
+  int64_t ldh;
+  uint4* hc;
+  uint4* dh;       // backward
+  int chunks;
 };
 
-// Compact row numbers of the counted tokens in token order, and their
-// targets; in the backward also their gradients and lse. One workgroup: a
-// thread counts and then numbers a run of consecutive tokens.
-__global__ void __launch_bounds__(1024) k_vocab_rows(const RowsArgs a) {
-  __shared__ int wsum[16];
+// Gathers the counted tokens' rows of h to the front of hc in token order, with
+// their targets and, in the backward, their gradients and lse; a token that is
+// not counted gets zeros in its row of dh. A workgroup does `per` tokens (a
+// multiple of 64) and finds its first compact row by counting the targets
+// before its own, all workgroups at the same time: no launch before this one,
+// and at most 1024 workgroups read the targets.
+__global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per) {
+  __shared__ int red[2][4];
+  __shared__ int pos[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.T + 1023) / 1024;
-  const int t0 = min(a.T, tid * per), t1 = min(a.T, t0 + per);
-  int mine = 0;
-  for (int t = t0; t < t1; ++t) {
+  const int t0 = blockIdx.x * per, t1 = min(a.T, t0 + per);
+  int before = 0, total = 0;
+#pragma unroll 4
+  for (int t = tid; t < a.T; t += 256) {
     const int64_t y = a.target[t];
-    mine += y >= 0 && y < a.V;
+    const int c = y >= 0 && y < a.V;
+    total += c;
+    before += t < t0 ? c : 0;
   }
-  int before = mine;  // inclusive scan over the wave
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(before, o);
-    if (lane >= o) before += v;
+  for (int o = 32; o > 0; o >>= 1) {
+    before += __shfl_xor(before, o);
+    total += __shfl_xor(total, o);
   }
-  if (lane == 63) wsum[wave] = before;
+  if (lane == 0) {
+    red[0][wave] = before;
+    red[1][wave] = total;
+  }
   __syncthreads();
-  int total = 0, base = 0;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) {
-    if (w < wave) base += wsum[w];
-    total += wsum[w];
-  }
-  int c = base + before - mine;
+  int base = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+  total = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+  if (blockIdx.x == 0 && tid == 0) *a.r.count = total;
   const float mean = a.scale / static_cast<float>(total);
-  for (int t = t0; t < t1; ++t) {
-    const int64_t y = a.target[t];
+  for (int b = t0; b < t1; b += 64) {
+    // every wave numbers the 64 tokens alike; the first writes
+    const int t = b + lane;
+    const int64_t y = t < t1 ? a.target[t] : -1;
     const bool counted = y >= 0 && y < a.V;
-    a.r.pos[t] = counted ? c : -1;
-    if (counted) {
-      a.r.idx[c] = t;
-      a.r.tgt[c] = static_cast<int>(y);
-      if (a.lse_in) {
-        a.r.g[c] = a.dloss ? a.scale * a.dloss[t] : mean;
-        a.r.lse[c] = a.lse_in[t];
+    const unsigned long long m = __ballot(counted);
+    const int p = counted ? base + __popcll(m & ((1ull << lane) - 1)) : -1;
+    base += __popcll(m);
+    if (wave == 0 && t < t1) {
+      pos[lane] = p;
+      a.r.pos[t] = p;
+      if (counted) {
+        a.r.idx[p] = t;
+        a.r.tgt[p] = static_cast<int>(y);
+        if (a.lse_in) {
+          a.r.g[p] = a.dloss ? a.scale * a.dloss[t] : mean;
+          a.r.lse[p] = a.lse_in[t];
+        }
       }
-      ++c;
     }
+    __syncthreads();
+    const int n = min(64, t1 - b);
+    for (int i = wave; i < n; i += 4) {
+      const int to = pos[i];
+      if (to >= 0) {
+        const uint4* src = a.h + (b + i) * a.ldh;
+        uint4* dst = a.hc + static_cast<int64_t>(to) * a.chunks;
+        for (int c = lane; c < a.chunks; c += 64) dst[c] = src[c];
+      } else if (a.dh) {
+        uint4* dst = a.dh + static_cast<int64_t>(b + i) * a.chunks;
+        for (int c = lane; c < a.chunks; c += 64) dst[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    __syncthreads();
   }
-  if (tid == 0) *a.r.count = total;
 }
 
-// Row t of h to its compact row of hc (a token that is not counted: zeros to
-// its row of dh, if there is one). With `pad`, compact rows from the count to
-// T are zeroed too, by the workgroup of that number. 16-byte chunks.
-__global__ void __launch_bounds__(256) k_vocab_gather(const uint4* h, int64_t ldh, const int32_t* pos,
-                                                      const int32_t* count, uint4* hc, uint4* dh, int chunks, bool pad) {
-  const int64_t t = blockIdx.x;
-  const int p = pos[t];
-  const uint4 z = make_uint4(0, 0, 0, 0);
-  if (p >= 0) {
-    for (int c = threadIdx.x; c < chunks; c += 256) hc[static_cast<int64_t>(p) * chunks + c] = h[t * ldh + c];
-  } else if (dh) {
-    for (int c = threadIdx.x; c < chunks; c += 256) dh[t * chunks + c] = z;
-  }
-  if (pad && t >= *count)
-    for (int c = threadIdx.x; c < chunks; c += 256) hc[t * chunks + c] = z;
-}
-
-// --- bfloat16 tiles -----------------------------------------------------------
+// --- tiles ----------------------------------------------------------------------
 
 struct TileArgs {
   TileOperand A, B;
@@ -106,12 +117,22 @@ struct TileArgs {
   float2* stat;
   float* tl;
   // gradient of the logits
-  bf16_t* p;
+  void* p;
   int64_t ldp;
   // dh, dw
   float* acc32;
   int first, last;
-  bf16_t* out;
+  void* out;
+};
+
+// storage of a tile's element size
+template <int ES>
+struct Elem {
+  typedef bf16_t type;
+};
+template <>
+struct Elem<4> {
+  typedef float type;
 };
 
 // Tile index of the workgroup among the tiles of the counted rows; false past
@@ -157,30 +178,33 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
   float2* red = reinterpret_cast<float2*>(smem);  // [WN][BM]
+  // the first K group's waves hold the sums
+  if (wave < Cfg::NW) {
 #pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i) {
-    const int row = tile_row<Cfg>(wm, lane, i);
-    const int tcol = m0 + row < count ? a.r.tgt[m0 + row] - n0 : -1;
-    float m = -INFINITY, s = 0.f;
+    for (int i = 0; i < Cfg::TM; ++i) {
+      const int row = tile_row<Cfg>(wm, lane, i);
+      const int tcol = m0 + row < count ? a.r.tgt[m0 + row] - n0 : -1;
+      float m = -INFINITY, s = 0.f;
 #pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j)
+      for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int col = tile_col<Cfg>(wn, lane, j, r);
-        if (col == tcol) a.tl[m0 + row] = acc[i][j][r];
-        m = fmaxf(m, n0 + col < a.vn ? acc[i][j][r] : -INFINITY);
-      }
-    m *= kLog2e;
-    const float ref = m == -INFINITY ? 0.f : m;
+        for (int r = 0; r < 16; ++r) {
+          const int col = tile_col<Cfg>(wn, lane, j, r);
+          if (col == tcol) a.tl[m0 + row] = acc[i][j][r];
+          m = fmaxf(m, n0 + col < a.vn ? acc[i][j][r] : -INFINITY);
+        }
+      m *= kLog2e;
+      const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j)
+      for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int col = tile_col<Cfg>(wn, lane, j, r);
-        s += n0 + col < a.vn ? exp_rel(acc[i][j][r], ref) : 0.f;
-      }
-    join_stat(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
-    if (lane < 32) red[wn * Cfg::BM + row] = make_float2(m, s);
+        for (int r = 0; r < 16; ++r) {
+          const int col = tile_col<Cfg>(wn, lane, j, r);
+          s += n0 + col < a.vn ? exp_rel(acc[i][j][r], ref) : 0.f;
+        }
+      join_stat(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
+      if (lane < 32) red[wn * Cfg::BM + row] = make_float2(m, s);
+    }
   }
   __syncthreads();
   const int row = threadIdx.x;
@@ -216,8 +240,8 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
   loss[t] = c >= 0 ? l - tl[c] : 0.f;
 }
 
-// Gradient of the logits of a piece, rounded to bfloat16: p [count][ldp],
-// zero in the columns past the vocabulary.
+// Gradient of the logits of a piece in the storage type: p [count][ldp], zero
+// in the columns past the vocabulary.
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[Cfg::LDS];
@@ -236,8 +260,9 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
   for (int i = 0; i < Cfg::TM; ++i) {
     const int row = m0 + tile_row<Cfg>(wm, lane, i);
     const bool in = row < count;
-    const int tcol = in ? a.r.tgt[row] - a.v0 - n0 : -1;
-    const float ref = in ? a.r.lse[row] * kLog2e : 0.f, g = in ? a.r.g[row] : 0.f;
+    const int at = in ? row : m0;  // rows past the count are not stored
+    const int tcol = a.r.tgt[at] - a.v0 - n0;
+    const float ref = a.r.lse[at] * kLog2e, g = a.r.g[at];
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
@@ -248,7 +273,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
       }
   }
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
-    if (m0 + row < count) tile_store8(a.p + static_cast<int64_t>(m0 + row) * a.ldp + n0 + col, v);
+    if (m0 + row < count) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.p) + static_cast<int64_t>(m0 + row) * a.ldp + n0 + col, v);
   });
 }
 
@@ -277,7 +302,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
       o[0] += s0.x; o[1] += s0.y; o[2] += s0.z; o[3] += s0.w;
       o[4] += s1.x; o[5] += s1.y; o[6] += s1.z; o[7] += s1.w;
     }
-    if (a.last) tile_store8(a.out + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
+    if (a.last) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
     else tile_store8(sum, o);
   });
 }
@@ -297,83 +322,65 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
   tile_product<Cfg>(A, B, m0, n0, count, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int m = m0 + row, k = n0 + col;
-    if (m < a.vn && k < a.d) tile_store8(a.out + static_cast<int64_t>(a.v0 + m) * a.d + k, v);
+    if (m < a.vn && k < a.d) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.v0 + m) * a.d + k, v);
   });
 }
 
-// --- float32 -------------------------------------------------------------------
-
-// Running maximum and sum of every compact row over a piece of logits
-// p [T][ldp], columns [0, vn), and the targets' logits. A wave per row.
-__global__ void __launch_bounds__(256) k_vocab_stat_f32(const float* p, int64_t ldp, int v0, int vn, VocabRows r,
-                                                        float2* run, float* tl, int first) {
-  const int c = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (c >= *r.count) return;
-  const float* row = p + static_cast<int64_t>(c) * ldp;
-  float m = -INFINITY;
-  for (int v = lane; v < vn; v += 64) m = fmaxf(m, row[v]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  m *= kLog2e;
-  const float ref = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
-  for (int v = lane; v < vn; v += 64) s += exp_rel(row[v], ref);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-  if (lane) return;
-  const int tv = r.tgt[c] - v0;
-  if (tv >= 0 && tv < vn) tl[c] = row[tv];
-  if (!first) join_stat(m, s, run[c].x, run[c].y);
-  run[c] = make_float2(m, s);
-}
-
-__global__ void __launch_bounds__(256) k_vocab_join_f32(const float2* run, const float* tl, const int32_t* pos, int T,
-                                                        float* loss, float* lse) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= T) return;
-  const int c = pos[t];
-  const float l = c >= 0 ? (run[c].x + __builtin_amdgcn_logf(run[c].y)) * kLn2 : 0.f;
-  lse[t] = l;
-  loss[t] = c >= 0 ? l - tl[c] : 0.f;
-}
-
-// Logits of a piece to their gradient, in place; rows past the count zero.
-__global__ void __launch_bounds__(256) k_vocab_dlogits_f32(float* p, int64_t ldp, int v0, int vn, VocabRows r, int T) {
-  const int c = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (c >= T) return;
-  float* row = p + static_cast<int64_t>(c) * ldp;
-  if (c >= *r.count) {
-    for (int v = lane; v < vn; v += 64) row[v] = 0.f;
-    return;
-  }
-  const float ref = r.lse[c] * kLog2e, g = r.g[c];
-  const int tv = r.tgt[c] - v0;
-  for (int v = lane; v < vn; v += 64) row[v] = g * (exp_rel(row[v], ref) - (v == tv ? 1.f : 0.f));
-}
-
-// dh rows of the counted tokens from the sums
-__global__ void __launch_bounds__(256) k_vocab_scatter_f32(const float4* acc, VocabRows r, float4* dh, int chunks) {
-  const int64_t c = blockIdx.x;
-  if (c >= *r.count) return;
-  const int64_t t = r.idx[c];
-  for (int k = threadIdx.x; k < chunks; k += 256) dh[t * chunks + k] = acc[c * chunks + k];
-}
-
-template <bool KTAIL>
-using CfgLogits = TileCfg<2, 256, 256, 2, 4, 2, true, true, KTAIL>;
-using CfgDh = TileCfg<2, 256, 256, 2, 4, 2, true, false, false>;
-using CfgDw = TileCfg<2, 256, 256, 2, 4, 2, false, false, false>;
-
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 
-void rows_of(const VocabDesc& D, bool backward, hipStream_t st) {
-  const RowsArgs a{D.target, D.V, static_cast<int>(D.T), D.rows, backward ? D.lse_in : nullptr, D.dloss, D.scale};
-  hipLaunchKernelGGL(k_vocab_rows, dim3(1), dim3(1024), 0, st, a);
-  const int es = D.bf16 ? 2 : 4;
-  hipLaunchKernelGGL(k_vocab_gather, dim3(static_cast<unsigned>(D.T)), dim3(256), 0, st,
-                     static_cast<const uint4*>(D.h), D.ldh * es / 16, D.rows.pos, D.rows.count,
-                     static_cast<uint4*>(D.hc), static_cast<uint4*>(backward ? D.dh : nullptr),
-                     static_cast<int>(D.d * es / 16), !D.bf16);
+// The tiles of a product with M rows (tokens: at most M) and N columns, by
+// what a round of them over the 256 CUs costs: a round's time grows with K
+// alike for all, the factors are those of full rounds measured with the int8
+// product, whose tiles move the same bytes (10.7, 21.4, 35 and 64 us at 32
+// steps). float products are bound by the matrix instructions at any tile, and
+// take 128 x 128 where that fills the CUs.
+enum VocabTile { kTile64, kTile128, kTile256x128, kTile256 };
+VocabTile pick_tile(int64_t M, int64_t N, bool bf16) {
+  static constexpr struct {
+    int bm, bn;
+    double cost;
+  } kTiles[] = {{64, 64, 10.7}, {128, 128, 21.4}, {256, 128, 35.0}, {256, 256, 64.0}};
+  if (!bf16) return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTile128 : kTile64;
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const double cost = static_cast<double>((static_cast<int64_t>(tiles(M, kTiles[i].bm)) * tiles(N, kTiles[i].bn) + 255) / 256) * kTiles[i].cost;
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return static_cast<VocabTile>(best);
+}
+
+// f(config) for the element size and tile, K-contiguous operands or not
+template <bool AKC, bool BKC, bool KTAIL, class F>
+void with_tile(bool bf16, VocabTile t, F&& f) {
+  if (!bf16) {
+    if (t == kTile64) f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{});
+    else f(TileCfg<4, 128, 128, 2, 4, 3, AKC, BKC, KTAIL>{});
+    return;
+  }
+  switch (t) {
+    case kTile64: f(TileCfg<2, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
+    case kTile128: f(TileCfg<2, 128, 128, 2, 4, 4, AKC, BKC, KTAIL>{}); return;
+    case kTile256x128: f(TileCfg<2, 256, 128, 4, 2, 3, AKC, BKC, KTAIL>{}); return;
+    default: f(TileCfg<2, 256, 256, 2, 4, 2, AKC, BKC, KTAIL>{}); return;
+  }
+}
+template <class F>
+void with_logits_tile(bool bf16, VocabTile t, int64_t d, F&& f) {
+  if (d % (bf16 ? 64 : 32)) with_tile<true, true, true>(bf16, t, f);
+  else with_tile<true, true, false>(bf16, t, f);
+}
+
+void gather_rows(const VocabDesc& D, bool backward, hipStream_t st) {
+  const int es = D.bf16 ? 2 : 4, T = static_cast<int>(D.T);
+  const RowsArgs a{D.target, D.V, T, D.rows, backward ? D.lse_in : nullptr, D.dloss, D.scale,
+                   static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc),
+                   static_cast<uint4*>(backward ? D.dh : nullptr), static_cast<int>(D.d * es / 16)};
+  const int per = T <= 8192 ? 16 : (tiles(T, 1024) + 63) / 64 * 64;
+  hipLaunchKernelGGL(k_vocab_gather, dim3(tiles(T, per)), dim3(256), 0, st, a, per);
 }
 
 TileArgs tile_args(const VocabDesc& D) {
@@ -384,126 +391,70 @@ TileArgs tile_args(const VocabDesc& D) {
   return a;
 }
 
-// logits of vocabulary rows [v0, v0 + vn), all compact rows (float32 path)
-bool logits_f32(const VocabDesc& D, int64_t v0, int64_t vn, hipStream_t st) {
-  GemmDesc g;
-  g.A = D.hc;
-  g.lda = D.d;
-  g.B = static_cast<const float*>(D.w) + v0 * D.ldw;
-  g.ldb = D.ldw;
-  g.C = D.p;
-  g.ldc = D.piece;
-  g.M = static_cast<int>(D.T);
-  g.N = static_cast<int>(vn);
-  g.K = static_cast<int>(D.d);
-  return gemm_f32(g, A_KCONTIG, B_KCONTIG, st);
-}
-
 }  // namespace
 
-bool vocab_forward(const VocabDesc& D, hipStream_t st) {
-  rows_of(D, false, st);
-  const int T = static_cast<int>(D.T);
-  if (D.bf16) {
-    TileArgs a = tile_args(D);
-    a.A = {D.hc, D.d, D.T, D.d};
-    a.B = {D.w, D.ldw, D.V, D.d};
-    a.vn = static_cast<int>(D.V);
-    a.tiles_n = tiles(D.V, 256);
-    a.stat = D.stat;
-    a.tl = D.tl;
-    const dim3 grid(static_cast<unsigned>(tiles(D.T, 256)) * a.tiles_n);
-    if (D.d % 64) hipLaunchKernelGGL((k_vocab_stat<CfgLogits<true>>), grid, dim3(512), 0, st, a);
-    else hipLaunchKernelGGL((k_vocab_stat<CfgLogits<false>>), grid, dim3(512), 0, st, a);
-    hipLaunchKernelGGL(k_vocab_join, dim3(tiles(D.T, 64)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
-                       D.loss, D.lse);
-    return true;
-  }
-  for (int64_t v0 = 0; v0 < D.V; v0 += D.piece) {
-    const int64_t vn = D.V - v0 < D.piece ? D.V - v0 : D.piece;
-    if (!logits_f32(D, v0, vn, st)) return false;
-    hipLaunchKernelGGL(k_vocab_stat_f32, dim3(tiles(D.T, 4)), dim3(256), 0, st, static_cast<const float*>(D.p),
-                       D.piece, static_cast<int>(v0), static_cast<int>(vn), D.rows, D.run, D.tl, v0 == 0);
-  }
-  hipLaunchKernelGGL(k_vocab_join_f32, dim3(tiles(D.T, 256)), dim3(256), 0, st, D.run, D.tl, D.rows.pos, T, D.loss,
-                     D.lse);
-  return true;
+int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
+  const VocabTile t = pick_tile(T, V, bf16);
+  return tiles(V, t == kTile64 ? 64 : (t == kTile256 ? 256 : 128));
 }
 
-bool vocab_backward(const VocabDesc& D, hipStream_t st) {
-  rows_of(D, true, st);
+void vocab_forward(const VocabDesc& D, hipStream_t st) {
+  gather_rows(D, false, st);
+  const int T = static_cast<int>(D.T);
+  TileArgs a = tile_args(D);
+  a.A = {D.hc, D.d, D.T, D.d};
+  a.B = {D.w, D.ldw, D.V, D.d};
+  a.vn = static_cast<int>(D.V);
+  a.stat = D.stat;
+  a.tl = D.tl;
+  with_logits_tile(D.bf16, pick_tile(D.T, D.V, D.bf16), D.d, [&](auto cfg) {
+    using C = decltype(cfg);
+    a.tiles_n = tiles(D.V, C::BN);
+    hipLaunchKernelGGL((k_vocab_stat<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+  });
+  hipLaunchKernelGGL(k_vocab_join, dim3(tiles(D.T, 64)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
+                     D.loss, D.lse);
+}
+
+void vocab_backward(const VocabDesc& D, hipStream_t st) {
+  gather_rows(D, true, st);
+  const int T = static_cast<int>(D.T), es = D.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < D.V; v0 += D.piece) {
     const int64_t vn = D.V - v0 < D.piece ? D.V - v0 : D.piece;
-    const bool first = v0 == 0, last = v0 + vn >= D.V;
-    if (D.bf16) {
-      const bf16_t* w = static_cast<const bf16_t*>(D.w) + v0 * D.ldw;
-      TileArgs a = tile_args(D);
-      a.v0 = static_cast<int>(v0);
-      a.vn = static_cast<int>(vn);
-      a.first = first;
-      a.last = last;
-      a.p = static_cast<bf16_t*>(D.p);
-      a.ldp = D.piece;
-      a.acc32 = D.acc;
-      const int tmT = tiles(D.T, 256);
-      // dl
-      a.A = {D.hc, D.d, D.T, D.d};
-      a.B = {w, D.ldw, vn, D.d};
-      a.tiles_n = tiles(vn, 256);
-      const dim3 grid(static_cast<unsigned>(tmT) * a.tiles_n);
-      if (D.d % 64) hipLaunchKernelGGL((k_vocab_dlogits<CfgLogits<true>>), grid, dim3(512), 0, st, a);
-      else hipLaunchKernelGGL((k_vocab_dlogits<CfgLogits<false>>), grid, dim3(512), 0, st, a);
-      // dh: the columns of p up to the next multiple of 64 are zero, and so
-      // are rows past the operand's end
-      a.A = {D.p, D.piece, D.T, D.piece};
-      a.B = {w, D.ldw, vn, D.d};
-      a.tiles_n = tiles(D.d, 256);
-      a.out = static_cast<bf16_t*>(D.dh);
-      hipLaunchKernelGGL((k_vocab_dh<CfgDh>), dim3(static_cast<unsigned>(tmT) * a.tiles_n), dim3(512), 0, st, a);
-      // dw
-      a.A = {D.p, D.piece, D.T, D.piece};
-      a.B = {D.hc, D.d, D.T, D.d};
-      a.out = static_cast<bf16_t*>(D.dw);
-      const int tmV = tiles(vn, 256);
-      hipLaunchKernelGGL((k_vocab_dw<CfgDw>), dim3(static_cast<unsigned>(tmV) * a.tiles_n), dim3(512), 0, st, a, tmV);
-      continue;
-    }
-    if (!logits_f32(D, v0, vn, st)) return false;
-    hipLaunchKernelGGL(k_vocab_dlogits_f32, dim3(tiles(D.T, 4)), dim3(256), 0, st, static_cast<float*>(D.p), D.piece,
-                       static_cast<int>(v0), static_cast<int>(vn), D.rows, static_cast<int>(D.T));
-    GemmDesc g;
-    g.A = D.p;
-    g.lda = D.piece;
-    g.B = static_cast<const float*>(D.w) + v0 * D.ldw;
-    g.ldb = D.ldw;
-    g.C = D.acc;
-    g.ldc = D.d;
-    g.M = static_cast<int>(D.T);
-    g.N = static_cast<int>(D.d);
-    g.K = static_cast<int>(vn);
-    if (!first) {
-      g.D = D.acc;
-      g.ldd = D.d;
-      g.beta = 1.f;
-    }
-    if (!gemm_f32(g, A_KCONTIG, B_NCONTIG, st)) return false;
-    GemmDesc u;
-    u.A = D.p;
-    u.lda = D.piece;
-    u.B = D.hc;
-    u.ldb = D.d;
-    u.C = static_cast<float*>(D.dw) + v0 * D.d;
-    u.ldc = D.d;
-    u.M = static_cast<int>(vn);
-    u.N = static_cast<int>(D.d);
-    u.K = static_cast<int>(D.T);
-    if (!gemm_f32(u, A_MCONTIG, B_NCONTIG, st)) return false;
+    const char* w = static_cast<const char*>(D.w) + v0 * D.ldw * es;
+    TileArgs a = tile_args(D);
+    a.v0 = static_cast<int>(v0);
+    a.vn = static_cast<int>(vn);
+    a.first = v0 == 0;
+    a.last = v0 + vn >= D.V;
+    a.p = D.p;
+    a.ldp = D.piece;
+    a.acc32 = D.acc;
+    a.A = {D.hc, D.d, D.T, D.d};
+    a.B = {w, D.ldw, vn, D.d};
+    with_logits_tile(D.bf16, pick_tile(D.T, vn, D.bf16), D.d, [&](auto cfg) {
+      using C = decltype(cfg);
+      a.tiles_n = tiles(vn, C::BN);
+      hipLaunchKernelGGL((k_vocab_dlogits<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+    });
+    // the columns of p up to the end of the last K step are zero, and so are
+    // rows past an operand's end
+    a.A = {D.p, D.piece, D.T, D.piece};
+    a.out = D.dh;
+    with_tile<true, false, false>(D.bf16, pick_tile(D.T, D.d, D.bf16), [&](auto cfg) {
+      using C = decltype(cfg);
+      a.tiles_n = tiles(D.d, C::BN);
+      hipLaunchKernelGGL((k_vocab_dh<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+    });
+    a.B = {D.hc, D.d, D.T, D.d};
+    a.out = D.dw;
+    with_tile<false, false, false>(D.bf16, pick_tile(vn, D.d, D.bf16), [&](auto cfg) {
+      using C = decltype(cfg);
+      a.tiles_n = tiles(D.d, C::BN);
+      const int tm = tiles(vn, C::BM);
+      hipLaunchKernelGGL((k_vocab_dw<C>), dim3(static_cast<unsigned>(tm) * a.tiles_n), dim3(C::NT), 0, st, a, tm);
+    });
   }
-  if (!D.bf16)
-    hipLaunchKernelGGL(k_vocab_scatter_f32, dim3(static_cast<unsigned>(D.T)), dim3(256), 0, st,
-                       reinterpret_cast<const float4*>(D.acc), D.rows, static_cast<float4*>(D.dh),
-                       static_cast<int>(D.d / 4));
-  return true;
 }
 
 }  // namespace poetx
