@@ -185,7 +185,7 @@ void linear_i8(const LinearI8Desc& d, hipStream_t st) {
     int bm, bn;
     double us;
   };
-  static constexpr Tile kTiles[] = {{64, 64, 10.7}, {64, 128, 15.5}, {128, 128, 21.4}, {256, 128, 35.0}, {256, 256, 64.0}};
+  static constexpr Tile kTiles[] = {{64, 64, 10.7}, {64, 128, 15.5}, {128, 128, 21.4}, {128, 256, 35.0}, {256, 256, 64.0}};
   int best = 0;
   double least = 0;
   for (int i = 0; i < 5; ++i) {
@@ -200,7 +200,7 @@ void linear_i8(const LinearI8Desc& d, hipStream_t st) {
     case 0: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
     case 1: launch_tail<64, 128, 2, 2, 4, 1>(a, d.out_bf16, st); return;
     case 2: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;
-    case 3: launch_tail<256, 128, 4, 2, 3, 1>(a, d.out_bf16, st); return;
+    case 3: launch_tail<128, 256, 2, 4, 3, 1>(a, d.out_bf16, st); return;
     default: launch_tail<256, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
   }
 }

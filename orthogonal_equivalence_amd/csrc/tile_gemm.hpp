@@ -118,7 +118,7 @@ __device__ __forceinline__ void tg_wait_vm() {
 // come two to a 256-byte bank window, wider ones one or less.
 template <int BT, int ES>
 __device__ __forceinline__ int row_swizzle(int r) {
-  if constexpr (ES == 4) return ((r >> 2) & 1) << 3;
+  if constexpr (ES == 4) return BT >= 64 ? ((r >> 2) & 1) << 3 : 0;
   else if constexpr (BT * ES == 128) return ((r >> 1) & 1) << 2;
   else return (r & 3) << 2;
 }

@@ -332,15 +332,19 @@ int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 // what a round of them over the 256 CUs costs: a round's time grows with K
 // alike for all, the factors are those of full rounds measured with the int8
 // product, whose tiles move the same bytes (10.7, 21.4, 35 and 64 us at 32
-// steps). float products are bound by the matrix instructions at any tile, and
-// take 128 x 128 where that fills the CUs.
-enum VocabTile { kTile64, kTile128, kTile256x128, kTile256 };
+// steps). float products are bound by the matrix instructions at any tile: 128 x
+// 128 where that fills the CUs, 32 x 32 where 64 x 64 would leave half of them
+// idle.
+enum VocabTile { kTile32, kTile64, kTile128, kTile128x256, kTile256 };
 VocabTile pick_tile(int64_t M, int64_t N, bool bf16) {
   static constexpr struct {
     int bm, bn;
     double cost;
-  } kTiles[] = {{64, 64, 10.7}, {128, 128, 21.4}, {256, 128, 35.0}, {256, 256, 64.0}};
-  if (!bf16) return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTile128 : kTile64;
+  } kTiles[] = {{64, 64, 10.7}, {128, 128, 21.4}, {128, 256, 35.0}, {256, 256, 64.0}};
+  if (!bf16) {
+    if (static_cast<int64_t>(tiles(M, 64)) * tiles(N, 64) < 128) return kTile32;
+    return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTile128 : kTile64;
+  }
   int best = 0;
   double least = 0;
   for (int i = 0; i < 4; ++i) {
@@ -350,21 +354,22 @@ VocabTile pick_tile(int64_t M, int64_t N, bool bf16) {
       least = cost;
     }
   }
-  return static_cast<VocabTile>(best);
+  return static_cast<VocabTile>(kTile64 + best);
 }
 
 // f(config) for the element size and tile, K-contiguous operands or not
 template <bool AKC, bool BKC, bool KTAIL, class F>
 void with_tile(bool bf16, VocabTile t, F&& f) {
   if (!bf16) {
-    if (t == kTile64) f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{});
+    if (t == kTile32) f(TileCfg<4, 32, 32, 1, 1, 2, AKC, BKC, KTAIL, 8>{});
+    else if (t == kTile64) f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{});
     else f(TileCfg<4, 128, 128, 2, 4, 3, AKC, BKC, KTAIL>{});
     return;
   }
   switch (t) {
     case kTile64: f(TileCfg<2, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
     case kTile128: f(TileCfg<2, 128, 128, 2, 4, 4, AKC, BKC, KTAIL>{}); return;
-    case kTile256x128: f(TileCfg<2, 256, 128, 4, 2, 3, AKC, BKC, KTAIL>{}); return;
+    case kTile128x256: f(TileCfg<2, 128, 256, 2, 4, 3, AKC, BKC, KTAIL>{}); return;
     default: f(TileCfg<2, 256, 256, 2, 4, 2, AKC, BKC, KTAIL>{}); return;
   }
 }
@@ -395,7 +400,7 @@ TileArgs tile_args(const VocabDesc& D) {
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
   const VocabTile t = pick_tile(T, V, bf16);
-  return tiles(V, t == kTile64 ? 64 : (t == kTile256 ? 256 : 128));
+  return tiles(V, t == kTile32 ? 32 : t == kTile64 ? 64 : t == kTile128 ? 128 : 256);
 }
 
 void vocab_forward(const VocabDesc& D, hipStream_t st) {
