@@ -1,6 +1,6 @@
 // int8 product with one scale per token and output: z[t][c] = xs[t] ws[c]
-// sum_k xq[t][k] wt[c][k], exact int32 sums on v_mfma_i32_32x32x32_i8, the
-// scales in the epilogue.
+// sum_k xq[t][k] wt[c][k], exact int32 sums on the matrix cores, the scales
+// in the epilogue.
 //
 // Many tokens are bound by the matrix cores and by the LDS that feeds them
 // (tile_gemm.hpp); in between, the K loop of a tile is a chain of latencies,
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_linear_i8(const I8Args a, int ti
   int tm, tn;
   tile_place(xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
-  i32x16_t acc[Cfg::TM][Cfg::TN];
+  i32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(a.x, a.w, m0, n0, a.m, 0, (a.m + Cfg::BK - 1) / Cfg::BK, smem, acc);
   O* z = static_cast<O*>(a.z);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {

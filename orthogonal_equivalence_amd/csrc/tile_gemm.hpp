@@ -3,25 +3,35 @@
 // tile of C per workgroup, left in registers for an epilogue of the caller's.
 //
 //  * Operands go global -> LDS with buffer loads that write LDS directly, 128
-//    bytes of K (64 bfloat16, 32 float, 128 int8) a step, NS stages, one barrier a
-//    step, a later stage's loads spread over the current stage's MFMAs. The
+//    bytes of K (64 bfloat16, 32 float, 128 int8) a step, NS stages. The
 //    buffer's record count ends at the operand's last byte, so rows past the
 //    end read as zero without an address select; with KTAIL, 16-byte chunks
 //    past the end of K get an offset outside the buffer for the same effect
 //    (what lies between rows may be anything, NaN too).
 //  * LDS rows of a K-contiguous operand are 128 bytes, chunk c of row r in
-//    slot c ^ (r & 7) ^ ((r >> 3) & 1): the 32 rows of a fragment read fall on
+//    slot c ^ (r & 7) ^ ((r >> 3) & 1): the 16 rows of a fragment read fall on
 //    all banks evenly.
 //  * An operand stored with K as its rows (A[k][m], B[k][n]) lies in LDS as it
 //    does in memory. bfloat16 is read with ds_read_b64_tr_b16, which hands
-//    every lane four consecutive k of its own column; chunk c of row r is in
-//    slot c ^ 4 (r & 3) (row_swizzle), so the four rows of a read fall in four
-//    different 64-byte quarters of the banks. float is read word by word, the two halves
-//    of a wave four rows apart; slot c ^ 8 ((r >> 2) & 1) keeps their banks
-//    apart.
-//  * The MFMA takes B's fragment first: a lane then holds, for one row m
-//    (lane % 32), groups of four consecutive columns n, and a row's reduction
-//    over columns stays within a lane and its partner lane ^ 32.
+//    every lane four consecutive k of its own column, float word by word;
+//    row_swizzle keeps the rows that one read touches on different banks.
+//  * 16 x 16 matrix instructions with 64 bytes of K (v_mfma_f32_16x16x32_bf16):
+//    under sustained load the chip's power limit, not the issue rate, bounds a
+//    large product, and they read and write the sums half as often as the 32 x
+//    32 ones. 8192 x 4096 x 16384 in bfloat16, a second of launches: 0.76 ms
+//    (1.45 PFLOP/s) against 0.82 ms; both 0.57 to 0.59 ms on all-zero inputs,
+//    where the chip does not throttle.
+//  * A K step has four phases: the two halves of a wave's rows for each 64
+//    bytes of K. Every phase reads the next one's fragments while its products
+//    run, across the barrier too: it comes before the last phase, whose
+//    fragments are in registers by then, and a stage's loads are issued in the
+//    last phase before it and the two after it, two products, one read and one
+//    load in turn. (One barrier at the top with the reads behind it: 0.87 ms.
+//    Four waves of 128 x 128 in place of eight of 128 x 64: 0.84 ms or more.
+//    Half steps in a ring of five slots: 0.89 ms. Wave priorities: 4% slower.)
+//  * The MFMA takes B's fragment first: a lane then holds, for one row m (lane
+//    % 16), groups of four consecutive columns n, and a row's reduction over
+//    columns stays within a lane and its partners lane ^ 16, lane ^ 32.
 #pragma once
 
 #include "common.hpp"
@@ -53,7 +63,7 @@ struct TileCfg {
   static constexpr int NW = WM * WN, NT = 64 * NW * KG;  // waves of a group, threads
   static constexpr int BK = 128 / ES;              // K of a step
   static constexpr int WTM = BM / WM, WTN = BN / WN;
-  static constexpr int TM = WTM / 32, TN = WTN / 32;
+  static constexpr int TM = WTM / 16, TN = WTN / 16, H = TM / 2;  // 16 x 16 tiles of a wave, row tiles of a phase
   static constexpr int ABYTES = BM * 128, BBYTES = BN * 128, STAGE = ABYTES + BBYTES;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads a wave
   static constexpr int SLAB = WTN + 8;             // epilogue slab row, floats
@@ -68,21 +78,13 @@ struct TileCfg {
 
 template <int ES>
 struct TileAcc {
-  typedef f32x16_t type;
-};
-template <>
-struct TileAcc<1> {
-  typedef i32x16_t type;
-};
-
-template <int ES>
-struct TileQuad {
   typedef f32x4_t type;
 };
 template <>
-struct TileQuad<1> {
+struct TileAcc<1> {
   typedef i32x4_t type;
 };
+
 template <int ES>
 struct TileFrag {
   typedef bf16x8_t type;
@@ -95,17 +97,17 @@ template <>
 struct TileFrag<4> {
   typedef f32x4_t type;
 };
-// eight k of a float fragment: four products of two
-__device__ __forceinline__ f32x16_t tile_mfma(f32x4_t a, f32x4_t b, f32x16_t c) {
+// sixteen k of a float fragment: four products of four
+__device__ __forceinline__ f32x4_t tile_mfma(f32x4_t a, f32x4_t b, f32x4_t c) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
   return c;
 }
-__device__ __forceinline__ f32x16_t tile_mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x4_t tile_mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ i32x16_t tile_mfma(i32x4_t a, i32x4_t b, i32x16_t c) {
-  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+__device__ __forceinline__ i32x4_t tile_mfma(i32x4_t a, i32x4_t b, i32x4_t c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
 template <int N>
@@ -113,14 +115,16 @@ __device__ __forceinline__ void tg_wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Slot of chunk c in row r of K of a tile of BT columns: c ^ row_swizzle(r),
-// the same for rows 4 (bfloat16) or 8 (float) further on. Rows of 128 bytes
-// come two to a 256-byte bank window, wider ones one or less.
+// Slot of chunk c in row r of K of a tile of BT columns: c ^ row_swizzle(r).
+// A transposed read takes 32 bytes each of rows 0 to 3 and 8 to 11 (then 16 to
+// 19 and 24 to 27) at a time: eight different 32-byte pieces of the 256-byte
+// bank window, which holds one row, or two of 128 bytes. A float read takes 64
+// bytes each of rows 0, 4, 8 and 12.
 template <int BT, int ES>
 __device__ __forceinline__ int row_swizzle(int r) {
-  if constexpr (ES == 4) return BT >= 64 ? ((r >> 2) & 1) << 3 : 0;
-  else if constexpr (BT * ES == 128) return ((r >> 1) & 1) << 2;
-  else return (r & 3) << 2;
+  if constexpr (ES == 4) return BT >= 64 ? ((r >> 2) & 3) << 2 : ((r >> 2) & 1) << 2;
+  else if constexpr (BT * ES == 128) return (((r >> 1) & 1) << 2) ^ (((r >> 3) & 1) << 1);
+  else return ((r & 3) << 2) ^ (((r >> 3) & 1) << 1);
 }
 
 // The loads of one operand tile: per-lane byte offsets from the tile's first
@@ -175,88 +179,103 @@ struct TileLoader {
 };
 
 // Transposed-read address (bytes in the operand's tile) of a lane for the
-// 32-column fragment at column `col0`, first 16 rows of K.
+// 16-column fragment at column `col0`, first 32 rows of K: lane group G reads
+// rows 8 G .. 8 G + 7, its lane i addressing row i / 4, column 4 (i % 4).
 template <int BT>
 __device__ __forceinline__ uint32_t tr_addr(int col0, int lane) {
-  const int grp = lane >> 4, li = lane & 15;
-  const int r = 8 * (grp >> 1) + (li >> 2);
-  const int col = col0 + 16 * (grp & 1) + 4 * (li & 3);
+  const int li = lane & 15;
+  const int r = 8 * (lane >> 4) + (li >> 2);
+  const int col = col0 + 4 * (li & 3);
   return static_cast<uint32_t>(r * BT * 2 + (((col >> 3) ^ row_swizzle<BT, 2>(r)) << 4) + (col & 7) * 2);
 }
 
-// One, two or four bfloat16 fragments by transposed reads; each asm block
-// waits for its own results (as builtins the reads would wait for the direct
-// loads in flight).
+// bfloat16 fragments by transposed reads, rows +4 in the second read of each;
+// an asm block waits for its own results (as builtins the reads would wait for
+// the direct loads in flight).
+typedef unsigned long long tr_u64;
+typedef unsigned long long tr_u64x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ bf16x8_t tr_frag(tr_u64 lo, tr_u64 hi) {
+  return __builtin_bit_cast(bf16x8_t, tr_u64x2{lo, hi});
+}
+#define POETX_TR(lo, hi, ad, off) \
+  "ds_read_b64_tr_b16 %" #lo ", %" #ad "\n ds_read_b64_tr_b16 %" #hi ", %" #ad " offset:%" #off "\n"
 template <int BT>
-__device__ __forceinline__ void tr_read(const uint32_t (&a)[1], uint32_t off, bf16x8_t (&f)[1]) {
-  typedef unsigned long long u64;
-  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-  u64 r[2];
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %2\n ds_read_b64_tr_b16 %1, %2 offset:%3\n"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r[0]), "=&v"(r[1])
-      : "v"(a[0] + off), "n"(4 * BT * 2)
-      : "memory");
-  f[0] = __builtin_bit_cast(bf16x8_t, u64x2{r[0], r[1]});
+__device__ __forceinline__ void tr_read(const uint32_t* a, uint32_t off, bf16x8_t (&f)[1]) {
+  tr_u64 r[2];
+  asm volatile(POETX_TR(0, 1, 2, 3) "s_waitcnt lgkmcnt(0)"
+               : "=&v"(r[0]), "=&v"(r[1])
+               : "v"(a[0] + off), "n"(4 * BT * 2)
+               : "memory");
+  f[0] = tr_frag(r[0], r[1]);
 }
 template <int BT>
-__device__ __forceinline__ void tr_read(const uint32_t (&a)[2], uint32_t off, bf16x8_t (&f)[2]) {
-  typedef unsigned long long u64;
-  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-  u64 r[4];
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %4\n ds_read_b64_tr_b16 %1, %4 offset:%6\n"
-      "ds_read_b64_tr_b16 %2, %5\n ds_read_b64_tr_b16 %3, %5 offset:%6\n"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
-      : "v"(a[0] + off), "v"(a[1] + off), "n"(4 * BT * 2)
-      : "memory");
-  f[0] = __builtin_bit_cast(bf16x8_t, u64x2{r[0], r[1]});
-  f[1] = __builtin_bit_cast(bf16x8_t, u64x2{r[2], r[3]});
-}
-template <int BT>
-__device__ __forceinline__ void tr_read(const uint32_t (&a)[4], uint32_t off, bf16x8_t (&f)[4]) {
-  typedef unsigned long long u64;
-  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-  u64 r[8];
-  asm volatile(
-      "ds_read_b64_tr_b16 %0, %8\n ds_read_b64_tr_b16 %1, %8 offset:%12\n"
-      "ds_read_b64_tr_b16 %2, %9\n ds_read_b64_tr_b16 %3, %9 offset:%12\n"
-      "ds_read_b64_tr_b16 %4, %10\n ds_read_b64_tr_b16 %5, %10 offset:%12\n"
-      "ds_read_b64_tr_b16 %6, %11\n ds_read_b64_tr_b16 %7, %11 offset:%12\n"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
-      : "v"(a[0] + off), "v"(a[1] + off), "v"(a[2] + off), "v"(a[3] + off), "n"(4 * BT * 2)
-      : "memory");
+__device__ __forceinline__ void tr_read(const uint32_t* a, uint32_t off, bf16x8_t (&f)[2]) {
+  tr_u64 r[4];
+  asm volatile(POETX_TR(0, 1, 4, 6) POETX_TR(2, 3, 5, 6) "s_waitcnt lgkmcnt(0)"
+               : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+               : "v"(a[0] + off), "v"(a[1] + off), "n"(4 * BT * 2)
+               : "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = __builtin_bit_cast(bf16x8_t, u64x2{r[2 * i], r[2 * i + 1]});
+  for (int i = 0; i < 2; ++i) f[i] = tr_frag(r[2 * i], r[2 * i + 1]);
 }
+template <int BT>
+__device__ __forceinline__ void tr_read(const uint32_t* a, uint32_t off, bf16x8_t (&f)[4]) {
+  tr_u64 r[8];
+  asm volatile(POETX_TR(0, 1, 8, 12) POETX_TR(2, 3, 9, 12) POETX_TR(4, 5, 10, 12) POETX_TR(6, 7, 11, 12)
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]),
+                 "=&v"(r[7])
+               : "v"(a[0] + off), "v"(a[1] + off), "v"(a[2] + off), "v"(a[3] + off), "n"(4 * BT * 2)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = tr_frag(r[2 * i], r[2 * i + 1]);
+}
+// four fragments each of two operands under one wait
+template <int BTA, int BTB>
+__device__ __forceinline__ void tr_read(const uint32_t* a, uint32_t offa, bf16x8_t (&fa)[4], const uint32_t* b,
+                                        uint32_t offb, bf16x8_t (&fb)[4]) {
+  tr_u64 r[8], s[8];
+  asm volatile(POETX_TR(0, 1, 16, 24) POETX_TR(2, 3, 17, 24) POETX_TR(4, 5, 18, 24) POETX_TR(6, 7, 19, 24)
+               POETX_TR(8, 9, 20, 25) POETX_TR(10, 11, 21, 25) POETX_TR(12, 13, 22, 25) POETX_TR(14, 15, 23, 25)
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]),
+                 "=&v"(r[7]), "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3]), "=&v"(s[4]), "=&v"(s[5]),
+                 "=&v"(s[6]), "=&v"(s[7])
+               : "v"(a[0] + offa), "v"(a[1] + offa), "v"(a[2] + offa), "v"(a[3] + offa), "v"(b[0] + offb),
+                 "v"(b[1] + offb), "v"(b[2] + offb), "v"(b[3] + offb), "n"(4 * BTA * 2), "n"(4 * BTB * 2)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    fa[i] = tr_frag(r[2 * i], r[2 * i + 1]);
+    fb[i] = tr_frag(s[2 * i], s[2 * i + 1]);
+  }
+}
+#undef POETX_TR
 
 // Address of a lane's column in the fragment of float rows at column col0:
-// rows 8 kk + 4 (lane / 32) + e, e = 0..3, of K group kk. The rows' slots are
-// those of row 4 (lane / 32) in every group.
+// rows 16 kk + 4 (lane / 16) + e, e = 0..3, of K group kk; the rows' slots do
+// not depend on kk or e.
 template <int BT>
 __device__ __forceinline__ uint32_t row_addr_f32(int col0, int lane) {
-  const int half = lane >> 5, col = col0 + (lane & 31);
-  return static_cast<uint32_t>(half * 4 * BT * 4 + (((col >> 2) ^ row_swizzle<BT, 4>(half * 4)) << 4) + (col & 3) * 4);
+  const int r = 4 * (lane >> 4), col = col0 + (lane & 15);
+  return static_cast<uint32_t>(r * BT * 4 + (((col >> 2) ^ row_swizzle<BT, 4>(r)) << 4) + (col & 3) * 4);
 }
 template <int BT, int N>
-__device__ __forceinline__ void row_read(const char* tile, const uint32_t (&a)[N], int kk, f32x4_t (&f)[N]) {
+__device__ __forceinline__ void row_read(const char* tile, const uint32_t* a, int kk, f32x4_t (&f)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[i][e] = *reinterpret_cast<const float*>(tile + a[i] + (kk * 8 + e) * BT * 4);
+    for (int e = 0; e < 4; ++e) f[i][e] = *reinterpret_cast<const float*>(tile + a[i] + (kk * 16 + e) * BT * 4);
 }
 
-// The wave's TM x TN tiles of 32 x 32 of the workgroup's tile at (m0, n0),
+// The wave's TM x TN tiles of 16 x 16 of the workgroup's tile at (m0, n0),
 // over K steps [it0, it1) of a K of `K` elements. smem: Cfg::LDS bytes, free
 // again for the caller when this returns (after its barrier).
 template <class Cfg>
 __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOperand& B, int m0, int n0, int64_t K,
                                              int it0, int it1, char* lds,
                                              typename TileAcc<Cfg::ES>::type (&acc)[Cfg::TM][Cfg::TN]) {
-  constexpr int TM = Cfg::TM, TN = Cfg::TN, LA = Cfg::LA, LB = Cfg::LB;
+  constexpr int TM = Cfg::TM, TN = Cfg::TN, H = Cfg::H, LA = Cfg::LA, LB = Cfg::LB;
   const int lane = threadIdx.x & 63;
   const int gwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = gwave % Cfg::NW, group = gwave / Cfg::NW;
@@ -274,105 +293,137 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = 0;
   if (it0 >= it1) {
     __syncthreads();
     return;
   }
 
-  // fragment addresses: K group kk of a K-contiguous row is chunk 2 kk +
-  // lane / 32 (32 bytes of K)
-  const int lrow = lane & 31;
+  // fragment addresses: K group kk of a K-contiguous row is chunk 4 kk +
+  // lane / 16 (64 bytes of K)
+  const int lrow = lane & 15;
   const int sw = (lrow & 7) ^ ((lrow >> 3) & 1);
-  int koff[4];
+  int koff[2];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) koff[kk] = lrow * 128 + (((2 * kk + (lane >> 5)) ^ sw) << 4);
+  for (int kk = 0; kk < 2; ++kk) koff[kk] = lrow * 128 + (((4 * kk + (lane >> 4)) ^ sw) << 4);
   const int abase = wm * Cfg::WTM * 128, bbase = Cfg::ABYTES + wn * Cfg::WTN * 128;
   uint32_t acol[Cfg::AKC ? 1 : TM], bcol[Cfg::BKC ? 1 : TN];
   if constexpr (!Cfg::AKC) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int col = wm * Cfg::WTM + i * 32;
+      const int col = wm * Cfg::WTM + i * 16;
       acol[i] = Cfg::ES == 2 ? tr_addr<Cfg::BM>(col, lane) : row_addr_f32<Cfg::BM>(col, lane);
     }
   }
   if constexpr (!Cfg::BKC) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int col = wn * Cfg::WTN + j * 32;
+      const int col = wn * Cfg::WTN + j * 16;
       bcol[j] = Cfg::ABYTES + (Cfg::ES == 2 ? tr_addr<Cfg::BN>(col, lane) : row_addr_f32<Cfg::BN>(col, lane));
     }
   }
 
+  // half h of the rows' fragments for K group kk, and the columns' fragments
   typedef typename TileFrag<Cfg::ES>::type Frag;
-  auto read = [&](const char* st, int kk, Frag(&fa)[TM], Frag(&fb)[TN]) {
+  auto read_a = [&](const char* st, int kk, int h, Frag(&f)[H]) {
     const uint32_t sb = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(st));
     if constexpr (Cfg::AKC) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const Frag*>(st + abase + i * 32 * 128 + koff[kk]);
+      for (int i = 0; i < H; ++i) f[i] = *reinterpret_cast<const Frag*>(st + abase + (h * H + i) * 16 * 128 + koff[kk]);
     } else if constexpr (Cfg::ES == 2) {
-      tr_read<Cfg::BM>(acol, sb + kk * 16 * Cfg::BM * 2, fa);
+      tr_read<Cfg::BM>(acol + h * H, sb + kk * 32 * Cfg::BM * 2, f);
     } else {
-      row_read<Cfg::BM, TM>(st, acol, kk, fa);
+      row_read<Cfg::BM, H>(st, acol + h * H, kk, f);
     }
+  };
+  auto read_b = [&](const char* st, int kk, Frag(&f)[TN]) {
+    const uint32_t sb = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(st));
     if constexpr (Cfg::BKC) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = *reinterpret_cast<const Frag*>(st + bbase + j * 32 * 128 + koff[kk]);
+      for (int j = 0; j < TN; ++j) f[j] = *reinterpret_cast<const Frag*>(st + bbase + j * 16 * 128 + koff[kk]);
     } else if constexpr (Cfg::ES == 2) {
-      tr_read<Cfg::BN>(bcol, sb + kk * 16 * Cfg::BN * 2, fb);
+      tr_read<Cfg::BN>(bcol, sb + kk * 32 * Cfg::BN * 2, f);
     } else {
-      row_read<Cfg::BN, TN>(st, bcol, kk, fb);
+      row_read<Cfg::BN, TN>(st, bcol, kk, f);
+    }
+  };
+  auto read_ab = [&](const char* st, int kk, Frag(&fa)[H], Frag(&fb)[TN]) {
+    if constexpr (Cfg::ES == 2 && !Cfg::AKC && !Cfg::BKC && H == 4 && TN == 4) {
+      const uint32_t sb = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(st));
+      tr_read<Cfg::BM, Cfg::BN>(acol, sb + kk * 32 * Cfg::BM * 2, fa, bcol, sb + kk * 32 * Cfg::BN * 2, fb);
+    } else {
+      read_b(st, kk, fb);
+      read_a(st, kk, 0, fa);
     }
   };
 
-  // steps past the last load the last slice again, into stages that are idle
-  // by then, so that the same number of loads is always in flight
-#pragma unroll
-  for (int s = 0; s < Cfg::NS - 1; ++s) {
-    const int pf = min(it0 + s * Cfg::KG + group, it1 - 1);
+  // The loads of a stage: N3 in the last phase of the step that frees its
+  // slot, the others in the next step's first. Steps past the last
+  // load the last slice again, into slots that are idle by then, so that the
+  // same number of loads is always in flight.
+  constexpr int L = LA + LB, N3 = (L + 1) / 2;
+  auto step_of = [&](int it) { return min(it + group, it1 - 1); };
+  auto load = [&](int i, int pf, char* to) {
     const int64_t kleft = Kb - static_cast<int64_t>(pf) * 128;
+    if (i < LA) la.load(i, pf, kleft, to, wave);
+    else lb.load(i - LA, pf, kleft, to + Cfg::ABYTES, wave);
+  };
 #pragma unroll
-    for (int i = 0; i < LA; ++i) la.load(i, pf, kleft, smem + s * Cfg::STAGE, wave);
+  for (int s = 0; s < Cfg::NS; ++s)
 #pragma unroll
-    for (int i = 0; i < LB; ++i) lb.load(i, pf, kleft, smem + s * Cfg::STAGE + Cfg::ABYTES, wave);
-  }
+    for (int i = 0; i < (s < Cfg::NS - 1 ? L : N3); ++i) load(i, step_of(it0 + s * Cfg::KG), smem + s * Cfg::STAGE);
+  tg_wait_vm<(Cfg::NS - 2) * L + N3>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frag af[2][H], bf[2][TN];
+  read_ab(smem, 0, af[0], bf[0]);
 
   int cur = 0;
   for (int it = it0; it < it1; it += Cfg::KG) {
-    // this step's loads are the oldest; a bare barrier (__syncthreads would
-    // wait for the younger ones too)
-    tg_wait_vm<(Cfg::NS - 2) * (LA + LB)>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const char* st = smem + cur * Cfg::STAGE;
-    char* nxt = smem + (cur == 0 ? Cfg::NS - 1 : cur - 1) * Cfg::STAGE;
-    cur = cur == Cfg::NS - 1 ? 0 : cur + 1;
-    const int pf = min(it + (Cfg::NS - 1) * Cfg::KG + group, it1 - 1);
     const bool mine = Cfg::KG == 1 || it + group < it1;  // a group may have no step left
-    const int64_t kleft = Kb - static_cast<int64_t>(pf) * 128;
-    Frag af[2][TM], bf[2][TN];
-    read(st, 0, af[0], bf[0]);
+    char* const st = smem + cur * Cfg::STAGE;
+    char* const prev = smem + (cur == 0 ? Cfg::NS - 1 : cur - 1) * Cfg::STAGE;
+    cur = cur == Cfg::NS - 1 ? 0 : cur + 1;
+    const char* const nxt = smem + cur * Cfg::STAGE;
+    const int pf = step_of(it + (Cfg::NS - 1) * Cfg::KG), pf2 = step_of(it + Cfg::NS * Cfg::KG);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      constexpr int L = LA + LB;
-      const int first = L == 8 ? (kk == 0 ? 0 : kk == 1 ? 2 : kk == 2 ? 5 : 8) : kk * L / 4;
-      const int last = L == 8 ? (kk == 0 ? 2 : kk == 1 ? 5 : 8) : (kk + 1) * L / 4;
-#pragma unroll
-      for (int i = 0; i < L; ++i)
-        if (i >= first && i < last) {
-          if (i < LA) la.load(i, pf, kleft, nxt, wave);
-          else lb.load(i - LA, pf, kleft, nxt + Cfg::ABYTES, wave);
-        }
-      // the next group's fragments are on their way while this group's
-      // products run
-      if (kk < 3) read(st, kk + 1, af[(kk + 1) & 1], bf[(kk + 1) & 1]);
+    for (int ph = 0; ph < 4; ++ph) {
+      const int kk = ph >> 1, h = ph & 1;
       __builtin_amdgcn_sched_barrier(0);
+      if (ph == 3) {
+        // this stage's reads are done and the next stage's loads (the oldest)
+        // have landed, in every wave after the barrier; a bare one
+        // (__syncthreads would wait for the younger loads too)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        tg_wait_vm<(Cfg::NS - 2) * L>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < N3; ++i) load(i, pf2, st);
+        read_ab(nxt, 0, af[0], bf[0]);
+      } else {
+        constexpr int N0 = L - N3;
+        const int first = ph == 0 ? N3 : L, last = ph == 0 ? N3 + N0 : L;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (i >= first && i < last) load(i, pf, prev);
+        if (ph == 0) read_a(st, 0, 1, af[1]);
+        else if (ph == 1) read_ab(st, 1, af[0], bf[1]);
+        else read_a(st, 1, 1, af[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          if (mine) acc[i][j] = tile_mfma(bf[kk & 1][j], af[kk & 1][i], acc[i][j]);
+          if (mine) acc[h * H + i][j] = tile_mfma(bf[kk][j], af[h][i], acc[h * H + i][j]);
+      if constexpr (H * TN >= 16) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, H * TN / 8, 0);  // products
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);           // loads
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -380,18 +431,15 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
   tg_wait_vm<0>();
   __syncthreads();
   if constexpr (Cfg::KG > 1) {
-    // [group - 1][wave][tile][quad of registers][lane], 16 bytes a lane
-    typedef typename TileQuad<Cfg::ES>::type Quad;
-    Quad* const join = reinterpret_cast<Quad*>(lds) + wave * TM * TN * 256 + lane;
+    // [group - 1][wave][tile][lane], 16 bytes a lane
+    typedef typename TileAcc<Cfg::ES>::type Acc;
+    Acc* const join = reinterpret_cast<Acc*>(lds) + wave * TM * TN * 64 + lane;
+    constexpr int GROUP = Cfg::NW * TM * TN * 64;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (group > 0)
-            join[(group - 1) * Cfg::NW * TM * TN * 256 + (i * TN + j) * 256 + q * 64] =
-                Quad{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (group > 0) join[(group - 1) * GROUP + (i * TN + j) * 64] = acc[i][j];
     __syncthreads();
     if (group == 0) {
 #pragma unroll
@@ -399,13 +447,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const Quad v = join[(g - 1) * Cfg::NW * TM * TN * 256 + (i * TN + j) * 256 + q * 64];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-            }
+          for (int j = 0; j < TN; ++j) acc[i][j] += join[(g - 1) * GROUP + (i * TN + j) * 64];
     }
     __syncthreads();
   }
@@ -414,11 +456,11 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
 // Row and column (of the workgroup's tile) of register r of tile (i, j) of a lane
 template <class Cfg>
 __device__ __forceinline__ int tile_row(int wm, int lane, int i) {
-  return wm * Cfg::WTM + i * 32 + (lane & 31);
+  return wm * Cfg::WTM + i * 16 + (lane & 15);
 }
 template <class Cfg>
 __device__ __forceinline__ int tile_col(int wn, int lane, int j, int r) {
-  return wn * Cfg::WTN + j * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
+  return wn * Cfg::WTN + j * 16 + (lane >> 4) * 4 + r;
 }
 
 // Hands the wave's values, as float, row by row through its LDS slab to
@@ -433,14 +475,15 @@ __device__ __forceinline__ void tile_rows(const typename TileAcc<Cfg::ES>::type 
   float* slab = reinterpret_cast<float*>(smem) + wave * 32 * Cfg::SLAB;
   constexpr int CPR = Cfg::WTN / 8, CPL = 32 * CPR / 64;
 #pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i) {
+  for (int i = 0; i < Cfg::TM / 2; ++i) {
 #pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4*>(slab + (lane & 31) * Cfg::SLAB + j * 32 + q * 8 + (lane >> 5) * 4) =
-            make_float4(static_cast<float>(acc[i][j][4 * q]), static_cast<float>(acc[i][j][4 * q + 1]),
-                        static_cast<float>(acc[i][j][4 * q + 2]), static_cast<float>(acc[i][j][4 * q + 3]));
+      for (int j = 0; j < Cfg::TN; ++j) {
+        const auto& v = acc[2 * i + u][j];
+        *reinterpret_cast<float4*>(slab + (u * 16 + (lane & 15)) * Cfg::SLAB + j * 16 + (lane >> 4) * 4) =
+            make_float4(static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]), static_cast<float>(v[3]));
+      }
     // the slab is the wave's own: its LDS accesses complete in order
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll

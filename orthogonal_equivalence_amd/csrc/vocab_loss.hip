@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
-  f32x16_t acc[Cfg::TM][Cfg::TN];
+  f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, a.B, m0, n0, a.d, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < 4; ++r) {
           const int col = tile_col<Cfg>(wn, lane, j, r);
           if (col == tcol) a.tl[m0 + row] = acc[i][j][r];
           m = fmaxf(m, n0 + col < a.vn ? acc[i][j][r] : -INFINITY);
@@ -198,12 +198,13 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < 4; ++r) {
           const int col = tile_col<Cfg>(wn, lane, j, r);
           s += n0 + col < a.vn ? exp_rel(acc[i][j][r], ref) : 0.f;
         }
+      join_stat(m, s, __shfl_xor(m, 16), __shfl_xor(s, 16));
       join_stat(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
-      if (lane < 32) red[wn * Cfg::BM + row] = make_float2(m, s);
+      if (lane < 16) red[wn * Cfg::BM + row] = make_float2(m, s);
     }
   }
   __syncthreads();
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
-  f32x16_t acc[Cfg::TM][Cfg::TN];
+  f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, a.B, m0, n0, a.d, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
+      for (int r = 0; r < 4; ++r) {
         const int col = tile_col<Cfg>(wn, lane, j, r);
         const float e = exp_rel(acc[i][j][r], ref) - (col == tcol ? 1.f : 0.f);
         acc[i][j][r] = n0 + col < a.vn ? g * e : 0.f;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
-  f32x16_t acc[Cfg::TM][Cfg::TN];
+  f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, a.B, m0, n0, a.vn, 0, (a.vn + Cfg::BK - 1) / Cfg::BK, smem, acc);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int c = m0 + row, k = n0 + col;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
   TileOperand A = a.A, B = a.B;
   A.rows = count;
   B.rows = count;
-  f32x16_t acc[Cfg::TM][Cfg::TN];
+  f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, B, m0, n0, count, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int m = m0 + row, k = n0 + col;
