@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_linear_i8(const I8Args a, int ti
   tile_place(xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, tm, tn);
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   i32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(a.x, a.w, m0, n0, a.m, 0, (a.m + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  tile_product<Cfg>(a.x, a.w, m0, n0, 0, (a.m + Cfg::BK - 1) / Cfg::BK, smem, acc);
   O* z = static_cast<O*>(a.z);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int t = m0 + row, c = n0 + col;
@@ -85,11 +85,10 @@ __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
   const int pieces = (a.m + 127) / 128;
   // past the last piece nothing is in range: zeros, no memory read
   auto load = [&](int p, char* to) {
-    const int64_t kleft = a.m - static_cast<int64_t>(p) * 128;
 #pragma unroll
-    for (int i = 0; i < 4 * OB; ++i) lw.load(i, p, kleft, to, 0);
+    for (int i = 0; i < 4 * OB; ++i) lw.load(i, p, to, 0);
 #pragma unroll
-    for (int i = 0; i < 4 * TT; ++i) lx.load(i, p, kleft, to + 4096 * OB, 0);
+    for (int i = 0; i < 4 * TT; ++i) lx.load(i, p, to + 4096 * OB, 0);
   };
 
   i32x16_t acc[TT][OB];
@@ -179,28 +178,12 @@ void linear_i8(const LinearI8Desc& d, hipStream_t st) {
     launch_few<1, 2, 4, 3>(a, d.out_bf16, st);
     return;
   }
-  // The tile whose rounds over the 256 CUs cost least. A round's time (us) as
-  // measured at m = 4096 with every CU at work; it grows with m alike for all.
-  struct Tile {
-    int bm, bn;
-    double us;
-  };
-  static constexpr Tile kTiles[] = {{64, 64, 10.7}, {64, 128, 15.5}, {128, 128, 21.4}, {128, 256, 35.0}, {256, 256, 64.0}};
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < 5; ++i) {
-    const int64_t tiles = int64_t((a.T + kTiles[i].bm - 1) / kTiles[i].bm) * ((a.n + kTiles[i].bn - 1) / kTiles[i].bn);
-    const double us = static_cast<double>((tiles + 255) / 256) * kTiles[i].us;
-    if (i == 0 || us < least) {
-      best = i;
-      least = us;
-    }
-  }
-  switch (best) {
-    case 0: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
-    case 1: launch_tail<64, 128, 2, 2, 4, 1>(a, d.out_bf16, st); return;
-    case 2: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;
-    case 3: launch_tail<128, 256, 2, 4, 3, 1>(a, d.out_bf16, st); return;
+  switch (pick_tile(a.T, a.n)) {
+    case kTile64x2: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
+    case kTile64: launch_tail<64, 64, 2, 2, 4, 1>(a, d.out_bf16, st); return;
+    case kTile128: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;
+    case kTile128x256: launch_tail<128, 256, 2, 4, 3, 1>(a, d.out_bf16, st); return;
+    case kTile192x256: launch_tail<192, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
     default: launch_tail<256, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
   }
 }

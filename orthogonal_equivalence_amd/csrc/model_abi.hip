@@ -94,7 +94,8 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.rows.g = bwd ? c.take<float>(T) : nullptr;
   v.rows.lse = bwd ? c.take<float>(T) : nullptr;
   v.rows.count = c.take<int32_t>(1);
-  v.hc = c.take<char>(T * D->d * es);
+  v.ldhc = (D->d * es + 127) / 128 * 128 / es;
+  v.hc = c.take<char>(T * v.ldhc * es);
   if (bwd) {
     v.p = c.take<char>(T * v.piece * es);
     if (v.piece < D->V) v.acc = c.take<float>(T * D->d);

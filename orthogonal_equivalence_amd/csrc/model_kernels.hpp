@@ -78,7 +78,8 @@ struct VocabDesc {
   int64_t T = 0, d = 0, V = 0;
   bool bf16 = true;
   VocabRows rows{};
-  void* hc = nullptr;       // [T][d] compact rows of h
+  void* hc = nullptr;       // [T][ldhc] compact rows of h
+  int64_t ldhc = 0;         // whole 128-byte lines, so that a tile's rows take no more lines than they fill
   // forward
   float2* stat = nullptr;   // [vocab_stat_tiles][T] maximum and sum of a tile's columns
   float* tl = nullptr;      // [T] target's logit of a compact row

@@ -42,6 +42,34 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int tg_u32x4_t __attribute__((ext_vector_type(4)));
 
+// The tiles of 1- and 2-byte products. A product takes the tile whose rounds
+// over the CUs cost least: a round's time, measured with the int8 product at
+// 32 K steps (m = 4096) and every slot taken, in us; it grows with K alike for
+// all. Small tiles are chains of latencies, and more of them at once hide each
+// other's (64 x 64 over two groups of waves, or two workgroups a CU).
+enum TileKind { kTile64x2, kTile64, kTile128, kTile128x256, kTile192x256, kTile256, kTileKinds };
+struct TileCost {
+  int bm, bn, slots;
+  double us;
+};
+constexpr TileCost kTileCosts[kTileKinds] = {{64, 64, 256, 11.2},   {64, 64, 512, 16.8},   {128, 128, 256, 22.0},
+                                             {128, 256, 256, 35.0}, {192, 256, 256, 46.5}, {256, 256, 256, 57.0}};
+inline TileKind pick_tile(int64_t M, int64_t N, bool no_192 = false) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < kTileKinds; ++i) {
+    if (no_192 && i == kTile192x256) continue;
+    const TileCost& t = kTileCosts[i];
+    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    const double us = static_cast<double>((tiles + t.slots - 1) / t.slots) * t.us;
+    if (i == 0 || us < least) {
+      best = i;
+      least = us;
+    }
+  }
+  return static_cast<TileKind>(best);
+}
+
 // One operand: rows of K (K-contiguous), or rows of columns with K down.
 // `rows`: rows of the stored matrix, `cols`: its row length, `ld`: row
 // stride, both in elements.
@@ -70,6 +98,7 @@ struct TileCfg {
   static constexpr int SLABS = NW * 32 * SLAB * 4;
   static constexpr int RING = NS * STAGE;
   static constexpr int JOIN = (KG - 1) * BM * BN * 4;
+  static_assert(BM % (16 * WM) == 0 && TM % 2 == 0 && BN % (16 * WN) == 0, "16 x 16 tiles in two halves");
   static constexpr int LDS = KG * RING > SLABS ? (KG * RING > JOIN ? KG * RING : JOIN) : (SLABS > JOIN ? SLABS : JOIN);
   static_assert((AKC || BM * ES >= 128) && (BKC || BN * ES >= 128), "rows of K of whole bank quarters");
   static_assert(ES != 1 || (AKC && BKC), "no transposed reads of bytes");
@@ -135,10 +164,13 @@ struct TileLoader {
   int64_t left;         // bytes from there to the operand's end
   int64_t kstep;        // bytes a K step advances
   uint32_t voff[L];
-  uint32_t kchunk[KC && KTAIL ? L : 1];  // byte of K of the lane's chunk
+  uint32_t vtail[KC && KTAIL ? L : 1];  // the same in the step that K ends in: chunks past it outside the buffer
+  int tail;                              // that step
 
   __device__ __forceinline__ void init(const TileOperand& o, int row0, int k0, int wave, int lane) {
     const int64_t ldb = o.ld * ES;
+    const int kend = static_cast<int>((o.cols - k0) * ES % 128);
+    tail = kend ? static_cast<int>((o.cols - k0) * ES / 128) : -1;
     if constexpr (KC) {
       base = static_cast<const char*>(o.p) + row0 * ldb + static_cast<int64_t>(k0) * ES;
       left = (o.rows - 1 - row0) * ldb + (o.cols - k0) * ES;
@@ -148,7 +180,7 @@ struct TileLoader {
         const int r = (wave * L + i) * 8 + (lane >> 3);
         const int c = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
         voff[i] = static_cast<uint32_t>(r * ldb) + c * 16;
-        if constexpr (KTAIL) kchunk[i] = c * 16;
+        if constexpr (KTAIL) vtail[i] = c * 16 < kend ? voff[i] : 0xfffffff0u;
       }
     } else {
       constexpr int RB = BT * ES, CH = RB / 16, RPI = 64 / CH;
@@ -164,15 +196,14 @@ struct TileLoader {
     }
   }
 
-  // load i of K step `it` into the operand's tile at `lds`; kleft: bytes of K
-  // from the step's start (KTAIL)
-  __device__ __forceinline__ void load(int i, int it, int64_t kleft, char* lds, int wave) const {
+  // load i of K step `it` into the operand's tile at `lds`
+  __device__ __forceinline__ void load(int i, int it, char* lds, int wave) const {
     const int64_t adv = it * kstep;
     const int64_t rem = left - adv;
     const uint32_t num = rem <= 0 ? 0u : (rem > 0x7fffffff ? 0x7fffffffu : static_cast<uint32_t>(rem));
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + adv), 0, static_cast<int>(num), 0x00020000);
     uint32_t v = voff[i];
-    if constexpr (KC && KTAIL) v = kchunk[i] < kleft ? v : 0xfffffff0u;
+    if constexpr (KC && KTAIL) v = it == tail ? vtail[i] : v;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * L + i) * 1024), 16, static_cast<int>(v), 0, 0, 0);
   }
@@ -269,10 +300,10 @@ __device__ __forceinline__ void row_read(const char* tile, const uint32_t* a, in
 }
 
 // The wave's TM x TN tiles of 16 x 16 of the workgroup's tile at (m0, n0),
-// over K steps [it0, it1) of a K of `K` elements. smem: Cfg::LDS bytes, free
+// over K steps [it0, it1). smem: Cfg::LDS bytes, free
 // again for the caller when this returns (after its barrier).
 template <class Cfg>
-__device__ __forceinline__ void tile_product(const TileOperand& A, const TileOperand& B, int m0, int n0, int64_t K,
+__device__ __forceinline__ void tile_product(const TileOperand& A, const TileOperand& B, int m0, int n0,
                                              int it0, int it1, char* lds,
                                              typename TileAcc<Cfg::ES>::type (&acc)[Cfg::TM][Cfg::TN]) {
   constexpr int TM = Cfg::TM, TN = Cfg::TN, H = Cfg::H, LA = Cfg::LA, LB = Cfg::LB;
@@ -281,7 +312,6 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
   const int wave = gwave % Cfg::NW, group = gwave / Cfg::NW;
   char* const smem = lds + group * Cfg::RING;
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
-  const int64_t Kb = K * Cfg::ES;
 
   TileLoader<Cfg::BM, LA, Cfg::AKC, Cfg::ES, Cfg::KTAIL> la;
   TileLoader<Cfg::BN, LB, Cfg::BKC, Cfg::ES, Cfg::KTAIL> lb;
@@ -364,9 +394,8 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
   constexpr int L = LA + LB, N3 = (L + 1) / 2;
   auto step_of = [&](int it) { return min(it + group, it1 - 1); };
   auto load = [&](int i, int pf, char* to) {
-    const int64_t kleft = Kb - static_cast<int64_t>(pf) * 128;
-    if (i < LA) la.load(i, pf, kleft, to, wave);
-    else lb.load(i - LA, pf, kleft, to + Cfg::ABYTES, wave);
+    if (i < LA) la.load(i, pf, to, wave);
+    else lb.load(i - LA, pf, to + Cfg::ABYTES, wave);
   };
 #pragma unroll
   for (int s = 0; s < Cfg::NS; ++s)
@@ -416,10 +445,10 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
 #pragma unroll
         for (int j = 0; j < TN; ++j)
           if (mine) acc[h * H + i][j] = tile_mfma(bf[kk][j], af[h][i], acc[h * H + i][j]);
-      if constexpr (H * TN >= 16) {
+      if constexpr (H * TN >= 12) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, H * TN / 8, 0);  // products
+          __builtin_amdgcn_sched_group_barrier(0x008, (H * TN + 4) / 8, 0);  // products
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS reads
           __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);           // loads
         }

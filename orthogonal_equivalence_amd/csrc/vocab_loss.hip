@@ -31,14 +31,15 @@ struct RowsArgs {
   const uint4* h;  // rows in 16-byte chunks
   int64_t ldh;
   uint4* hc;
+  int64_t ldhc;
   uint4* dh;       // backward
   int chunks;
 };
 
 // Gathers the counted tokens' rows of h to the front of hc in token order, with
 // their targets and, in the backward, their gradients and lse; a token that is
-// not counted gets zeros in its row of dh. A workgroup does `per` tokens (a
-// multiple of 64) and finds its first compact row by counting the targets
+// not counted gets zeros in its row of dh. A workgroup does `per` tokens, 64 at
+// a time, and finds its first compact row by counting the targets
 // before its own, all workgroups at the same time: no launch before this one,
 // and at most 1024 workgroups read the targets.
 __global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per)
       const int to = pos[i];
       if (to >= 0) {
         const uint4* src = a.h + (b + i) * a.ldh;
-        uint4* dst = a.hc + static_cast<int64_t>(to) * a.chunks;
+        uint4* dst = a.hc + to * a.ldhc;
         for (int c = lane; c < a.chunks; c += 64) dst[c] = src[c];
       } else if (a.dh) {
         uint4* dst = a.dh + static_cast<int64_t>(b + i) * a.chunks;
@@ -161,6 +162,21 @@ __device__ __forceinline__ void join_stat(float& m, float& s, float m2, float s2
   m = top;
 }
 
+// Columns of the tile from `left` on (past the vocabulary) set to v; nothing
+// to do in any but the last tile of a row.
+template <class Cfg>
+__device__ __forceinline__ void mask_columns(f32x4_t (&acc)[Cfg::TM][Cfg::TN], int wn, int lane, int left, float v) {
+  if (left >= Cfg::BN) return;
+#pragma unroll
+  for (int j = 0; j < Cfg::TN; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool past = tile_col<Cfg>(wn, lane, j, r) >= left;
+#pragma unroll
+      for (int i = 0; i < Cfg::TM; ++i) acc[i][j][r] = past ? v : acc[i][j][r];
+    }
+}
+
 // Maximum and sum of every row over the tile's columns, in powers of two, and
 // the targets' logits.
 template <class Cfg>
@@ -173,37 +189,40 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
   TileOperand A = a.A;
   A.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, a.B, m0, n0, a.d, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  tile_product<Cfg>(A, a.B, m0, n0, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
   float2* red = reinterpret_cast<float2*>(smem);  // [WN][BM]
   // the first K group's waves hold the sums
   if (wave < Cfg::NW) {
+    mask_columns<Cfg>(acc, wn, lane, a.vn - n0, -INFINITY);
 #pragma unroll
     for (int i = 0; i < Cfg::TM; ++i) {
       const int row = tile_row<Cfg>(wm, lane, i);
       const int tcol = m0 + row < count ? a.r.tgt[m0 + row] - n0 : -1;
-      float m = -INFINITY, s = 0.f;
+      if (__any(static_cast<unsigned>(tcol - wn * Cfg::WTN) < Cfg::WTN)) {
+#pragma unroll
+        for (int j = 0; j < Cfg::TN; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (tile_col<Cfg>(wn, lane, j, r) == tcol) a.tl[m0 + row] = acc[i][j][r];
+      }
+      float m = acc[i][0][0], s = 0.f;
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int col = tile_col<Cfg>(wn, lane, j, r);
-          if (col == tcol) a.tl[m0 + row] = acc[i][j][r];
-          m = fmaxf(m, n0 + col < a.vn ? acc[i][j][r] : -INFINITY);
-        }
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
       m *= kLog2e;
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int col = tile_col<Cfg>(wn, lane, j, r);
-          s += n0 + col < a.vn ? exp_rel(acc[i][j][r], ref) : 0.f;
-        }
-      join_stat(m, s, __shfl_xor(m, 16), __shfl_xor(s, 16));
-      join_stat(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
+        for (int r = 0; r < 4; ++r) s += exp_rel(acc[i][j][r], ref);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
       if (lane < 16) red[wn * Cfg::BM + row] = make_float2(m, s);
     }
   }
@@ -227,6 +246,7 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
   const int c = t < T ? pos[t] : -1;
   float m = -INFINITY, s = 0.f;
   if (c >= 0)
+#pragma unroll 4
     for (int k = wave; k < tiles; k += 16) {
       const float2 v = stat[static_cast<int64_t>(k) * T + c];
       join_stat(m, s, v.x, v.y);
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
   TileOperand A = a.A;
   A.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, a.B, m0, n0, a.d, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  tile_product<Cfg>(A, a.B, m0, n0, 0, (a.d + Cfg::BK - 1) / Cfg::BK, smem, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave % Cfg::WM, wn = wave / Cfg::WM;
@@ -267,12 +287,15 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int col = tile_col<Cfg>(wn, lane, j, r);
-        const float e = exp_rel(acc[i][j][r], ref) - (col == tcol ? 1.f : 0.f);
-        acc[i][j][r] = n0 + col < a.vn ? g * e : 0.f;
-      }
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = g * exp_rel(acc[i][j][r], ref);
+    if (__any(static_cast<unsigned>(tcol - wn * Cfg::WTN) < Cfg::WTN)) {
+#pragma unroll
+      for (int j = 0; j < Cfg::TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] -= tile_col<Cfg>(wn, lane, j, r) == tcol ? g : 0.f;
+    }
   }
+  mask_columns<Cfg>(acc, wn, lane, a.vn - n0, 0.f);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     if (m0 + row < count) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.p) + static_cast<int64_t>(m0 + row) * a.ldp + n0 + col, v);
   });
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
   TileOperand A = a.A;
   A.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, a.B, m0, n0, a.vn, 0, (a.vn + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  tile_product<Cfg>(A, a.B, m0, n0, 0, (a.vn + Cfg::BK - 1) / Cfg::BK, smem, acc);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int c = m0 + row, k = n0 + col;
     if (c >= count || k >= a.d) return;
@@ -320,7 +343,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
   A.rows = count;
   B.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, B, m0, n0, count, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  tile_product<Cfg>(A, B, m0, n0, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int m = m0 + row, k = n0 + col;
     if (m < a.vn && k < a.d) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.v0 + m) * a.d + k, v);
@@ -329,53 +352,42 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
 
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 
-// The tiles of a product with M rows (tokens: at most M) and N columns, by
-// what a round of them over the 256 CUs costs: a round's time grows with K
-// alike for all, the factors are those of full rounds measured with the int8
-// product, whose tiles move the same bytes (10.7, 21.4, 35 and 64 us at 32
-// steps). float products are bound by the matrix instructions at any tile: 128 x
-// 128 where that fills the CUs, 32 x 32 where 64 x 64 would leave half of them
+// float products are bound by the matrix instructions at any tile: 128 x 128
+// where that fills the CUs, 32 x 32 where 64 x 64 would leave half of them
 // idle.
-enum VocabTile { kTile32, kTile64, kTile128, kTile128x256, kTile256 };
-VocabTile pick_tile(int64_t M, int64_t N, bool bf16) {
-  static constexpr struct {
-    int bm, bn;
-    double cost;
-  } kTiles[] = {{64, 64, 10.7}, {128, 128, 21.4}, {128, 256, 35.0}, {256, 256, 64.0}};
-  if (!bf16) {
-    if (static_cast<int64_t>(tiles(M, 64)) * tiles(N, 64) < 128) return kTile32;
-    return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTile128 : kTile64;
-  }
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < 4; ++i) {
-    const double cost = static_cast<double>((static_cast<int64_t>(tiles(M, kTiles[i].bm)) * tiles(N, kTiles[i].bn) + 255) / 256) * kTiles[i].cost;
-    if (i == 0 || cost < least) {
-      best = i;
-      least = cost;
-    }
-  }
-  return static_cast<VocabTile>(kTile64 + best);
+enum TileKindF32 { kTileF32, kTileF64, kTileF128 };
+int pick(int64_t M, int64_t N, bool bf16, bool no_192 = false) {
+  if (bf16) return pick_tile(M, N, no_192);
+  if (static_cast<int64_t>(tiles(M, 64)) * tiles(N, 64) < 128) return kTileF32;
+  return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTileF128 : kTileF64;
 }
 
 // f(config) for the element size and tile, K-contiguous operands or not
 template <bool AKC, bool BKC, bool KTAIL, class F>
-void with_tile(bool bf16, VocabTile t, F&& f) {
+void with_tile(bool bf16, int t, F&& f) {
   if (!bf16) {
-    if (t == kTile32) f(TileCfg<4, 32, 32, 1, 1, 2, AKC, BKC, KTAIL, 8>{});
-    else if (t == kTile64) f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{});
-    else f(TileCfg<4, 128, 128, 2, 4, 3, AKC, BKC, KTAIL>{});
-    return;
+    switch (t) {
+      case kTileF32: f(TileCfg<4, 32, 32, 1, 1, 2, AKC, BKC, KTAIL, 8>{}); return;
+      case kTileF64: f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
+      default: f(TileCfg<4, 128, 128, 2, 4, 3, AKC, BKC, KTAIL>{}); return;
+    }
   }
   switch (t) {
-    case kTile64: f(TileCfg<2, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
+    case kTile64x2: f(TileCfg<2, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
+    case kTile64: f(TileCfg<2, 64, 64, 2, 2, 4, AKC, BKC, KTAIL>{}); return;
     case kTile128: f(TileCfg<2, 128, 128, 2, 4, 4, AKC, BKC, KTAIL>{}); return;
     case kTile128x256: f(TileCfg<2, 128, 256, 2, 4, 3, AKC, BKC, KTAIL>{}); return;
+    case kTile192x256:
+      if constexpr (AKC) {
+        f(TileCfg<2, 192, 256, 2, 4, 2, AKC, BKC, KTAIL>{});
+        return;
+      }
+      [[fallthrough]];
     default: f(TileCfg<2, 256, 256, 2, 4, 2, AKC, BKC, KTAIL>{}); return;
   }
 }
 template <class F>
-void with_logits_tile(bool bf16, VocabTile t, int64_t d, F&& f) {
+void with_logits_tile(bool bf16, int t, int64_t d, F&& f) {
   if (d % (bf16 ? 64 : 32)) with_tile<true, true, true>(bf16, t, f);
   else with_tile<true, true, false>(bf16, t, f);
 }
@@ -383,9 +395,9 @@ void with_logits_tile(bool bf16, VocabTile t, int64_t d, F&& f) {
 void gather_rows(const VocabDesc& D, bool backward, hipStream_t st) {
   const int es = D.bf16 ? 2 : 4, T = static_cast<int>(D.T);
   const RowsArgs a{D.target, D.V, T, D.rows, backward ? D.lse_in : nullptr, D.dloss, D.scale,
-                   static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc),
+                   static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc), D.ldhc * es / 16,
                    static_cast<uint4*>(backward ? D.dh : nullptr), static_cast<int>(D.d * es / 16)};
-  const int per = T <= 8192 ? 16 : (tiles(T, 1024) + 63) / 64 * 64;
+  const int per = T <= 2048 ? 4 : T <= 8192 ? 16 : (tiles(T, 1024) + 63) / 64 * 64;
   hipLaunchKernelGGL(k_vocab_gather, dim3(tiles(T, per)), dim3(256), 0, st, a, per);
 }
 
@@ -400,20 +412,20 @@ TileArgs tile_args(const VocabDesc& D) {
 }  // namespace
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
-  const VocabTile t = pick_tile(T, V, bf16);
-  return tiles(V, t == kTile32 ? 32 : t == kTile64 ? 64 : t == kTile128 ? 128 : 256);
+  const int t = pick(T, V, bf16);
+  return tiles(V, bf16 ? kTileCosts[t].bn : (t == kTileF32 ? 32 : (t == kTileF64 ? 64 : 128)));
 }
 
 void vocab_forward(const VocabDesc& D, hipStream_t st) {
   gather_rows(D, false, st);
   const int T = static_cast<int>(D.T);
   TileArgs a = tile_args(D);
-  a.A = {D.hc, D.d, D.T, D.d};
+  a.A = {D.hc, D.ldhc, D.T, D.d};
   a.B = {D.w, D.ldw, D.V, D.d};
   a.vn = static_cast<int>(D.V);
   a.stat = D.stat;
   a.tl = D.tl;
-  with_logits_tile(D.bf16, pick_tile(D.T, D.V, D.bf16), D.d, [&](auto cfg) {
+  with_logits_tile(D.bf16, pick(D.T, D.V, D.bf16), D.d, [&](auto cfg) {
     using C = decltype(cfg);
     a.tiles_n = tiles(D.V, C::BN);
     hipLaunchKernelGGL((k_vocab_stat<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
@@ -436,9 +448,9 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     a.p = D.p;
     a.ldp = D.piece;
     a.acc32 = D.acc;
-    a.A = {D.hc, D.d, D.T, D.d};
+    a.A = {D.hc, D.ldhc, D.T, D.d};
     a.B = {w, D.ldw, vn, D.d};
-    with_logits_tile(D.bf16, pick_tile(D.T, vn, D.bf16), D.d, [&](auto cfg) {
+    with_logits_tile(D.bf16, pick(D.T, vn, D.bf16), D.d, [&](auto cfg) {
       using C = decltype(cfg);
       a.tiles_n = tiles(vn, C::BN);
       hipLaunchKernelGGL((k_vocab_dlogits<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
@@ -447,14 +459,14 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     // rows past an operand's end
     a.A = {D.p, D.piece, D.T, D.piece};
     a.out = D.dh;
-    with_tile<true, false, false>(D.bf16, pick_tile(D.T, D.d, D.bf16), [&](auto cfg) {
+    with_tile<true, false, false>(D.bf16, pick(D.T, D.d, D.bf16), [&](auto cfg) {
       using C = decltype(cfg);
       a.tiles_n = tiles(D.d, C::BN);
       hipLaunchKernelGGL((k_vocab_dh<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
     });
-    a.B = {D.hc, D.d, D.T, D.d};
+    a.B = {D.hc, D.ldhc, D.T, D.d};
     a.out = D.dw;
-    with_tile<false, false, false>(D.bf16, pick_tile(vn, D.d, D.bf16), [&](auto cfg) {
+    with_tile<false, false, false>(D.bf16, pick(vn, D.d, D.bf16, true), [&](auto cfg) {
       using C = decltype(cfg);
       a.tiles_n = tiles(D.d, C::BN);
       const int tm = tiles(vn, C::BM);
