@@ -93,6 +93,7 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.rows.tgt = c.take<int32_t>(T);
   v.rows.g = bwd ? c.take<float>(T) : nullptr;
   v.rows.lse = bwd ? c.take<float>(T) : nullptr;
+  v.rows.unit = bwd ? c.take<float>(1) : nullptr;
   v.rows.count = c.take<int32_t>(1);
   v.ldhc = (D->d * es + 127) / 128 * 128 / es;
   v.hc = c.take<char>(T * v.ldhc * es);

@@ -65,7 +65,8 @@ struct VocabRows {
   int32_t* pos;    // [T]
   int32_t* idx;    // [T]
   int32_t* tgt;    // [T] target of compact row c
-  float* g;        // [T] upstream gradient of compact row c (backward)
+  float* g;        // [T] upstream gradient of compact row c, in units of the largest (backward)
+  float* unit;     // [1] that unit (backward)
   float* lse;      // [T] lse of compact row c (backward)
   int32_t* count;  // [1] counted tokens
 };

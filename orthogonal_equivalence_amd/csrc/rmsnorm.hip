@@ -412,26 +412,35 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_bwd(const NormBw
   }
 }
 
-// out[j] = sum over the groups, in a fixed order: 16 lanes of rows a column,
-// each over every 16th group, then a tree over the 16. Workgroups of 64
-// columns.
+// out[j] = sum over the groups, in a fixed order: 32 columns a workgroup, row
+// lane r of 32 over groups r, r + 32, .. (at most 32 of them, all loads in
+// flight), then a tree over the row lanes.
+constexpr int kMaxGroups = 1024;
 __global__ void __launch_bounds__(1024) k_dgain_sum(const float* part, int groups, int64_t n, float* out) {
-  __shared__ float s[16][64];
-  const int col = threadIdx.x & 63, lane = threadIdx.x >> 6;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + col;
+  __shared__ float s[32][33];
+  const int col = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + col;
   float v = 0.f;
   if (j < n) {
-#pragma unroll 8
-    for (int g = lane; g < groups; g += 16) v += part[static_cast<int64_t>(g) * n + j];
-  }
-  s[lane][col] = v;
-  __syncthreads();
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    if (lane < o) s[lane][col] += s[lane + o][col];
-    __syncthreads();
+    for (int k = 0; k < kMaxGroups / 32; k += 16) {
+      float u[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int g = (k + i) * 32 + r;
+        u[i] = g < groups ? part[static_cast<int64_t>(g) * n + j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v += u[i];
+    }
   }
-  if (lane == 0 && j < n) out[j] = s[0][col];
+  s[r][col] = v;
+  __syncthreads();
+  v = s[col][r];  // row lane `col` of column `r`
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  const int64_t to = static_cast<int64_t>(blockIdx.x) * 32 + r;
+  if (col == 0 && to < n) out[to] = v;
 }
 
 template <typename T, bool NORM, bool Q8>
@@ -486,7 +495,7 @@ void launch_bwd(const NormBwdArgs<T>& a, hipStream_t st) {
 
 int norm_bwd_groups(int64_t T, int64_t n) {
   const int64_t chunks = n / 8;
-  const int64_t most = chunks <= 128 ? 1024 : 512;
+  const int64_t most = chunks <= 128 ? kMaxGroups : kMaxGroups / 2;
   return static_cast<int>(T < most ? T : most);
 }
 
@@ -514,7 +523,7 @@ void norm_backward(const NormBwdDesc& d, hipStream_t st) {
   if (d.bf16) run(bf16_t{});
   else run(float{});
   if (d.part)
-    hipLaunchKernelGGL(k_dgain_sum, dim3(static_cast<unsigned>((d.n + 63) / 64)), dim3(1024), 0, st, d.part, groups, d.n,
+    hipLaunchKernelGGL(k_dgain_sum, dim3(static_cast<unsigned>((d.n + 31) / 32)), dim3(1024), 0, st, d.part, groups, d.n,
                        d.dgain);
 }
 

@@ -44,31 +44,40 @@ struct RowsArgs {
 // and at most 1024 workgroups read the targets.
 __global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per) {
   __shared__ int red[2][4];
+  __shared__ float redg[4];
   __shared__ int pos[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t0 = blockIdx.x * per, t1 = min(a.T, t0 + per);
   int before = 0, total = 0;
+  float most = 0.f;
 #pragma unroll 4
   for (int t = tid; t < a.T; t += 256) {
     const int64_t y = a.target[t];
     const int c = y >= 0 && y < a.V;
     total += c;
     before += t < t0 ? c : 0;
+    if (a.dloss && c) most = fmaxf(most, fabsf(a.dloss[t]));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     before += __shfl_xor(before, o);
     total += __shfl_xor(total, o);
+    most = fmaxf(most, __shfl_xor(most, o));
   }
   if (lane == 0) {
     red[0][wave] = before;
     red[1][wave] = total;
+    redg[wave] = most;
   }
   __syncthreads();
   int base = red[0][0] + red[0][1] + red[0][2] + red[0][3];
   total = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-  if (blockIdx.x == 0 && tid == 0) *a.r.count = total;
-  const float mean = a.scale / static_cast<float>(total);
+  // gradients in units of their largest: 1 for all of a mean loss's
+  most = fmaxf(fmaxf(redg[0], redg[1]), fmaxf(redg[2], redg[3]));
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.r.count = total;
+    if (a.lse_in) *a.r.unit = a.dloss ? a.scale * most : a.scale / static_cast<float>(max(total, 1));
+  }
   for (int b = t0; b < t1; b += 64) {
     // every wave numbers the 64 tokens alike; the first writes
     const int t = b + lane;
@@ -84,7 +93,7 @@ __global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per)
         a.r.idx[p] = t;
         a.r.tgt[p] = static_cast<int>(y);
         if (a.lse_in) {
-          a.r.g[p] = a.dloss ? a.scale * a.dloss[t] : mean;
+          a.r.g[p] = a.dloss ? (most == 0.f ? a.dloss[t] : a.dloss[t] / most) : 1.f;
           a.r.lse[p] = a.lse_in[t];
         }
       }
@@ -261,7 +270,11 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
   loss[t] = c >= 0 ? l - tl[c] : 0.f;
 }
 
-// Gradient of the logits of a piece in the storage type: p [count][ldp], zero
+// Gradient of the logits of a piece in the storage type, without the common
+// factor `unit`, which the products' epilogues put back in float32: a factor
+// rounded with the target's entries, which outweigh the rest, would shift all
+// of them alike (with g = 1 / count in bfloat16, 0.3% of dh and dw in place of
+// 0.17%). p [count][ldp], zero
 // in the columns past the vocabulary.
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) {
@@ -314,6 +327,7 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
   A.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, a.B, m0, n0, 0, (a.vn + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  const float unit = *a.r.unit;
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int c = m0 + row, k = n0 + col;
     if (c >= count || k >= a.d) return;
@@ -326,8 +340,13 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
       o[0] += s0.x; o[1] += s0.y; o[2] += s0.z; o[3] += s0.w;
       o[4] += s1.x; o[5] += s1.y; o[6] += s1.z; o[7] += s1.w;
     }
-    if (a.last) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
-    else tile_store8(sum, o);
+    if (a.last) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] *= unit;
+      tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
+    } else {
+      tile_store8(sum, o);
+    }
   });
 }
 
@@ -344,9 +363,14 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
   B.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
   tile_product<Cfg>(A, B, m0, n0, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  const float unit = *a.r.unit;
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int m = m0 + row, k = n0 + col;
-    if (m < a.vn && k < a.d) tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.v0 + m) * a.d + k, v);
+    if (m >= a.vn || k >= a.d) return;
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[i] * unit;
+    tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.v0 + m) * a.d + k, o);
   });
 }
 

@@ -78,6 +78,11 @@ def _call(name, dev, *args):
         raise px.PoetxError(name, st)
 
 
+def _like(t):
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _scratch(need, dev):
     return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
 
@@ -91,9 +96,9 @@ def rms_norm(x, gain, residual=None, eps=1e-6):
     ldx = _rows("x", x, x.shape, x.dtype, dev)
     ldr = _rows("residual", residual, x.shape, x.dtype, dev) if residual is not None else 0
     _flat("gain", gain, (n,), torch.float32, dev)
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    h = _like(x) if residual is not None else None
+    y = _like(x)
+    rstd = gain.new_empty(T)
     _call("poetx_rmsnorm_forward", dev, T, n, dt, x.data_ptr(), ldx, _ptr(residual), ldr, gain.data_ptr(), eps, _ptr(h),
           y.data_ptr(), rstd.data_ptr())
     return (h if h is not None else x), y, rstd
@@ -107,9 +112,9 @@ def rms_norm_q8(x, gain, residual=None, eps=1e-6):
     ldx = _rows("x", x, x.shape, x.dtype, dev)
     ldr = _rows("residual", residual, x.shape, x.dtype, dev) if residual is not None else 0
     _flat("gain", gain, (n,), torch.float32, dev)
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if residual is not None else None
+    h = _like(x) if residual is not None else None
     q = torch.empty((T, n), dtype=torch.int8, device=dev)
-    scale = torch.empty(T, dtype=torch.float32, device=dev)
+    scale = gain.new_empty(T)
     _call("poetx_rmsnorm_forward_q8", dev, T, n, dt, x.data_ptr(), ldx, _ptr(residual), ldr, gain.data_ptr(), eps,
           _ptr(h), q.data_ptr(), scale.data_ptr())
     return (h if h is not None else x), q, scale
@@ -140,8 +145,8 @@ def rms_norm_backward(dy, h, rstd, gain, dh=None):
     if dh is not None:
         dh = _grad(dh)
         lddh = _rows("dh", dh, dy.shape, dy.dtype, dev)
-    dx = torch.empty((T, n), dtype=dy.dtype, device=dev)
-    dgain = torch.empty(n, dtype=torch.float32, device=dev)
+    dx = _like(dy)
+    dgain = torch.empty_like(gain)
     need = mo.poetx_rmsnorm_ws_bytes(T, n)
     ws = _scratch(need, dev)
     _call("poetx_rmsnorm_backward", dev, T, n, dt, dy.data_ptr(), lddy, h.data_ptr(), rstd.data_ptr(), gain.data_ptr(),
@@ -204,7 +209,7 @@ def vocab_loss(h, w, target, piece=0):
     logits are not kept."""
     T, d, V, ldh, ldw, dev, D = _vocab(h, w, target, piece)
     loss = torch.empty(T, dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty_like(loss)
     need = mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_FORWARD)
     ws = _scratch(need, dev)
     _call("poetx_vocab_loss_forward", dev, D, T, h.data_ptr(), ldh, w.data_ptr(), ldw, target.data_ptr(),
@@ -222,8 +227,7 @@ def vocab_loss_backward(h, w, target, lse, dloss=None, scale=1.0, piece=0):
     if dloss is not None:
         dloss = _grad(dloss)
         _flat("dloss", dloss, (T,), torch.float32, dev)
-    dh = torch.empty((T, d), dtype=h.dtype, device=dev)
-    dw = torch.empty((V, d), dtype=h.dtype, device=dev)
+    dh, dw = _like(h), _like(w)
     need = mo.poetx_vocab_ws_bytes(D, T, mo.POETX_OP_VOCAB_BACKWARD)
     ws = _scratch(need, dev)
     _call("poetx_vocab_loss_backward", dev, D, T, h.data_ptr(), ldh, w.data_ptr(), ldw, target.data_ptr(),
