@@ -178,7 +178,7 @@ void linear_i8(const LinearI8Desc& d, hipStream_t st) {
     launch_few<1, 2, 4, 3>(a, d.out_bf16, st);
     return;
   }
-  switch (pick_tile(a.T, a.n)) {
+  switch (pick_tile(kTileCosts, kTileKinds, a.T, a.n)) {
     case kTile64x2: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
     case kTile64: launch_tail<64, 64, 2, 2, 4, 1>(a, d.out_bf16, st); return;
     case kTile128: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;

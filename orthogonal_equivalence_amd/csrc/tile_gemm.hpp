@@ -42,11 +42,11 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int tg_u32x4_t __attribute__((ext_vector_type(4)));
 
-// The tiles of 1- and 2-byte products. A product takes the tile whose rounds
-// over the CUs cost least: a round's time, measured with the int8 product at
-// 32 K steps (m = 4096) and every slot taken, in us; it grows with K alike for
-// all. Small tiles are chains of latencies, and more of them at once hide each
-// other's (64 x 64 over two groups of waves, or two workgroups a CU).
+// Tiles of a product: it takes the one whose rounds over the CUs cost least. A
+// round's time, measured with every slot taken, in us; it grows with K alike
+// for all. 1- and 2-byte products, as the int8 product at 32 K steps (m =
+// 4096): small tiles are chains of latencies, and more of them at once hide
+// each other's (64 x 64 over two groups of waves, or two workgroups a CU).
 enum TileKind { kTile64x2, kTile64, kTile128, kTile128x256, kTile192x256, kTile256, kTileKinds };
 struct TileCost {
   int bm, bn, slots;
@@ -54,20 +54,26 @@ struct TileCost {
 };
 constexpr TileCost kTileCosts[kTileKinds] = {{64, 64, 256, 11.2},   {64, 64, 512, 16.8},   {128, 128, 256, 22.0},
                                              {128, 256, 256, 35.0}, {192, 256, 256, 46.5}, {256, 256, 256, 57.0}};
-inline TileKind pick_tile(int64_t M, int64_t N, bool no_192 = false) {
-  int best = 0;
+// float products, per K step: nearly in proportion to the tile, as the matrix
+// instructions bound all of them.
+enum TileKindF32 { kTileF32, kTileF64, kTileF128, kTileKindsF32 };
+constexpr TileCost kTileCostsF32[kTileKindsF32] = {{32, 32, 256, 0.17}, {64, 64, 256, 0.60}, {128, 128, 256, 2.03}};
+
+// index of the cheapest of n tiles for an M x N product, without tile `skip`
+inline int pick_tile(const TileCost* tiles, int n, int64_t M, int64_t N, int skip = -1) {
+  int best = -1;
   double least = 0;
-  for (int i = 0; i < kTileKinds; ++i) {
-    if (no_192 && i == kTile192x256) continue;
-    const TileCost& t = kTileCosts[i];
-    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
-    const double us = static_cast<double>((tiles + t.slots - 1) / t.slots) * t.us;
-    if (i == 0 || us < least) {
+  for (int i = 0; i < n; ++i) {
+    if (i == skip) continue;
+    const TileCost& t = tiles[i];
+    const int64_t count = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    const double us = static_cast<double>((count + t.slots - 1) / t.slots) * t.us;
+    if (best < 0 || us < least) {
       best = i;
       least = us;
     }
   }
-  return static_cast<TileKind>(best);
+  return best;
 }
 
 // One operand: rows of K (K-contiguous), or rows of columns with K down.

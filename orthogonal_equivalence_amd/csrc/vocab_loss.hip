@@ -376,14 +376,11 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
 
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 
-// float products are bound by the matrix instructions at any tile: 128 x 128
-// where that fills the CUs, 32 x 32 where 64 x 64 would leave half of them
-// idle.
-enum TileKindF32 { kTileF32, kTileF64, kTileF128 };
+// (192 rows do not divide into the whole-row loads of an operand with K as its
+// rows, as dw's first one has)
 int pick(int64_t M, int64_t N, bool bf16, bool no_192 = false) {
-  if (bf16) return pick_tile(M, N, no_192);
-  if (static_cast<int64_t>(tiles(M, 64)) * tiles(N, 64) < 128) return kTileF32;
-  return static_cast<int64_t>(tiles(M, 128)) * tiles(N, 128) >= 256 ? kTileF128 : kTileF64;
+  if (bf16) return pick_tile(kTileCosts, kTileKinds, M, N, no_192 ? kTile192x256 : -1);
+  return pick_tile(kTileCostsF32, kTileKindsF32, M, N);
 }
 
 // f(config) for the element size and tile, K-contiguous operands or not
@@ -437,7 +434,7 @@ TileArgs tile_args(const VocabDesc& D) {
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
   const int t = pick(T, V, bf16);
-  return tiles(V, bf16 ? kTileCosts[t].bn : (t == kTileF32 ? 32 : (t == kTileF64 ? 64 : 128)));
+  return tiles(V, bf16 ? kTileCosts[t].bn : kTileCostsF32[t].bn);
 }
 
 void vocab_forward(const VocabDesc& D, hipStream_t st) {
