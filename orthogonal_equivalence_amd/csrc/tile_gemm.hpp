@@ -534,10 +534,10 @@ __device__ __forceinline__ void tile_rows(const typename TileAcc<Cfg::ES>::type 
   }
 }
 
-// Tile (tm, tn) of index pid: groups of 8 tile rows walked column by column,
+// Tile (tm, tn) of index pid: groups of 4 tile rows walked column by column,
 // so that neighbouring pids share operand panels.
 __device__ __forceinline__ void tile_place(int pid, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int GM = 8;
+  constexpr int GM = 4;
   const int group = GM * tiles_n;
   const int first = (pid / group) * GM;
   const int size = min(tiles_m - first, GM);

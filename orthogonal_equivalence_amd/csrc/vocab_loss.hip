@@ -105,7 +105,15 @@ __global__ void __launch_bounds__(256) k_vocab_gather(const RowsArgs a, int per)
       if (to >= 0) {
         const uint4* src = a.h + (b + i) * a.ldh;
         uint4* dst = a.hc + to * a.ldhc;
-        for (int c = lane; c < a.chunks; c += 64) dst[c] = src[c];
+        for (int c = lane; c < a.chunks; c += 512) {  // 8 KB in flight a wave
+          uint4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (c + u * 64 < a.chunks) v[u] = src[c + u * 64];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (c + u * 64 < a.chunks) dst[c + u * 64] = v[u];
+        }
       } else if (a.dh) {
         uint4* dst = a.dh + static_cast<int64_t>(b + i) * a.chunks;
         for (int c = lane; c < a.chunks; c += 64) dst[c] = make_uint4(0, 0, 0, 0);
