@@ -34,7 +34,8 @@ def _out(act):
 # every width class of the kernels and its edges, one token to many
 SHAPES = [(1, 8), (3, 16), (5, 504), (2, 512), (7, 520), (1, 1024), (9, 1032), (4, 2048), (3, 2056), (1, 4096),
           (6, 4104), (2, 8192), (3, 8200), (2, 16384), (1, 16392), (2, 32768), (2, 32776), (1, 70000), (1500, 72),
-          (1030, 1032), (600, 2064)]
+          (1030, 1032), (600, 2064), (7, 64), (9000, 64), (13, 128), (9001, 136), (4500, 256), (6, 264), (700, 6152),
+          (513, 8200)]
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
