@@ -161,7 +161,7 @@ void launch_few(const I8Args& a, bool bf16, hipStream_t st) {
 
 }  // namespace
 
-void linear_i8(const LinearI8Desc& d, hipStream_t st) {
+bool linear_i8(const LinearI8Desc& d, hipStream_t st) {
   const I8Args a{{d.xq, d.m, d.T, d.m}, {d.wt, d.m, d.n, d.m}, d.xs, d.ws, d.z, d.ldz,
                  static_cast<int>(d.T), static_cast<int>(d.n), static_cast<int>(d.m)};
   // Few tokens: one ring a wave. 64 outputs a workgroup where 32 would make
@@ -172,20 +172,23 @@ void linear_i8(const LinearI8Desc& d, hipStream_t st) {
   if (a.T <= 32) {
     if (a.n > 256 * 32) launch_few<2, 1, 4, 2>(a, d.out_bf16, st);
     else launch_few<1, 1, 4, 4>(a, d.out_bf16, st);
-    return;
+    return true;
   }
   if (a.T <= 64 && a.n <= 256 * 32) {
     launch_few<1, 2, 4, 3>(a, d.out_bf16, st);
-    return;
+    return true;
   }
-  switch (pick_tile(kTileCosts, kTileKinds, a.T, a.n)) {
-    case kTile64x2: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); return;
-    case kTile64: launch_tail<64, 64, 2, 2, 4, 1>(a, d.out_bf16, st); return;
-    case kTile128: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); return;
-    case kTile128x256: launch_tail<128, 256, 2, 4, 3, 1>(a, d.out_bf16, st); return;
-    case kTile192x256: launch_tail<192, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
-    default: launch_tail<256, 256, 2, 4, 2, 1>(a, d.out_bf16, st); return;
+  const int tile = pick_tile(kTileCosts, kTileKinds, a.T, a.n);
+  if (!tiles_fit(kTileCosts[tile], a.T, a.n)) return false;
+  switch (tile) {
+    case kTile64x2: launch_tail<64, 64, 2, 2, 3, 2>(a, d.out_bf16, st); break;
+    case kTile64: launch_tail<64, 64, 2, 2, 4, 1>(a, d.out_bf16, st); break;
+    case kTile128: launch_tail<128, 128, 2, 4, 4, 1>(a, d.out_bf16, st); break;
+    case kTile128x256: launch_tail<128, 256, 2, 4, 3, 1>(a, d.out_bf16, st); break;
+    case kTile192x256: launch_tail<192, 256, 2, 4, 2, 1>(a, d.out_bf16, st); break;
+    default: launch_tail<256, 256, 2, 4, 2, 1>(a, d.out_bf16, st); break;
   }
+  return true;
 }
 
 }  // namespace poetx

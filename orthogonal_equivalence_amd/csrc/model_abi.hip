@@ -111,7 +111,8 @@ int vocab_common(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t
   const int es = elem(D->dtype);
   if (!stride_ok(ldh, D->d, es) || !stride_ok(ldw, D->d, es)) return POETX_EINVAL;
   if (!ptrs_ok({h, w, target})) return POETX_EINVAL;
-  if (ldw > kVocabStride) return POETX_EUNSUPPORTED;
+  if (ldw > kVocabStride || !vocab_fits(T, D->d, D->V, piece_of(D, T), D->dtype == POETX_BF16))
+    return POETX_EUNSUPPORTED;
   return ws_ok(ws, ws_bytes, poetx_vocab_ws_bytes(D, T, op));
 }
 
@@ -239,7 +240,7 @@ int poetx_linear_i8(int64_t T, int64_t m, int64_t n, int out_dtype, const int8_t
   d.n = n;
   d.out_bf16 = out_dtype == POETX_BF16;
   ProfScope p("linear_i8", stream);
-  linear_i8(d, stream);
+  if (!linear_i8(d, stream)) return POETX_EUNSUPPORTED;
   return launch_status();
 }
 

@@ -56,7 +56,8 @@ struct LinearI8Desc {
   int64_t T = 0, m = 0, n = 0;
   bool out_bf16 = true;
 };
-void linear_i8(const LinearI8Desc& d, hipStream_t stream);
+// false, with nothing launched, where T and n make more tiles than one launch holds.
+bool linear_i8(const LinearI8Desc& d, hipStream_t stream);
 
 // Vocabulary cross entropy (poetx_vocab_loss_*). The counted tokens (target
 // in [0, V)) are gathered to the front: compact row c is token idx[c], and
@@ -96,6 +97,8 @@ struct VocabDesc {
   void* dh = nullptr;
   void* dw = nullptr;
 };
+// Whether every product's tiles fit one launch.
+bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
 // Column tiles of the forward.
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16);
 void vocab_forward(const VocabDesc& d, hipStream_t stream);

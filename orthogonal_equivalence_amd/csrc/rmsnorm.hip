@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_fwd(const NormAr
   __shared__ float red[2][16];
   int turn = 0;
   const int t = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR;
+  const int64_t row = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * RPW + threadIdx.x / TPR;
   if (row >= a.T_) return;  // a row's threads together; a row over several waves has the workgroup to itself
   const T* x = a.x + row * a.ldx;
   const T* r = a.res ? a.res + row * a.ldr : nullptr;
@@ -461,13 +461,20 @@ __global__ void __launch_bounds__(1024) k_dgain_sum(const float* part, int group
   if (col == 0 && to < n) out[to] = v;
 }
 
+// n workgroups of up to 1024 threads in two dimensions: the threads of one stay
+// below 2^32
+dim3 row_grid(int64_t n) {
+  constexpr int64_t kMost = int64_t(1) << 21;
+  return dim3(static_cast<unsigned>(n < kMost ? n : kMost), static_cast<unsigned>((n + kMost - 1) / kMost));
+}
+
 template <typename T, bool NORM, bool Q8>
 void launch_fwd(const NormArgs<T>& a, hipStream_t st) {
   const int64_t chunks = a.n / 8;
 #define POETX_NORM_FWD(TPR, CH)                                                                          \
   {                                                                                                      \
     constexpr int rpw = TPR < 256 ? 256 / TPR : 1;                                                       \
-    hipLaunchKernelGGL((k_norm_fwd<T, TPR, CH, NORM, Q8>), dim3(static_cast<unsigned>((a.T_ + rpw - 1) / rpw)), \
+    hipLaunchKernelGGL((k_norm_fwd<T, TPR, CH, NORM, Q8>), row_grid((a.T_ + rpw - 1) / rpw),              \
                        dim3(TPR < 256 ? 256 : TPR), 0, st, a);                                           \
     return;                                                                                              \
   }

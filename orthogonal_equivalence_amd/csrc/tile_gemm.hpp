@@ -76,6 +76,12 @@ inline int pick_tile(const TileCost* tiles, int n, int64_t M, int64_t N, int ski
   return best;
 }
 
+// A launch's threads in one dimension stay below 2^32: whether the chosen
+// tile's workgroups (of at most 512) do.
+inline bool tiles_fit(const TileCost& t, int64_t M, int64_t N) {
+  return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) < (int64_t(1) << 23);
+}
+
 // One operand: rows of K (K-contiguous), or rows of columns with K down.
 // `rows`: rows of the stored matrix, `cols`: its row length, `ld`: row
 // stride, both in elements.

@@ -14,6 +14,8 @@
 #include "model_kernels.hpp"
 #include "tile_gemm.hpp"
 
+#include <algorithm>
+
 namespace poetx {
 namespace {
 
@@ -439,6 +441,14 @@ TileArgs tile_args(const VocabDesc& D) {
 }
 
 }  // namespace
+
+bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
+  const TileCost* t = bf16 ? kTileCosts : kTileCostsF32;
+  const int64_t last = V % piece ? V % piece : piece;
+  for (int64_t vn : {std::min(V, piece), last})
+    if (!tiles_fit(t[pick(T, vn, bf16)], T, vn) || !tiles_fit(t[pick(vn, d, bf16, true)], vn, d)) return false;
+  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[pick(T, d, bf16)], T, d);
+}
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
   const int t = pick(T, V, bf16);

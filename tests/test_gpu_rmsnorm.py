@@ -204,6 +204,20 @@ def test_rows_past_two_to_the_31_elements():
     within("dgain", dgain, want, 1e-4 * want)
 
 
+def test_more_rows_than_one_grid_dimension_holds():
+    T, n = (1 << 24) + 5, 1040   # 2^24 workgroups of 256 threads are 2^32 threads
+    print(f"\n[gpu] quantize_rows T={T} n={n}", flush=True)
+    x = torch.zeros((T, n), dtype=torch.bfloat16, device="cuda")
+    for i in (0, (1 << 21) - 1, 1 << 21, 1 << 24, T - 1):
+        x[i, i % n] = 1 + i % 7
+    q, scale = model.quantize_rows(x)
+    torch.cuda.synchronize()
+    for i in (0, (1 << 21) - 1, 1 << 21, 1 << 24, T - 1):
+        assert int(q[i, i % n]) == 127 and int(q[i].abs().sum()) == 127
+        assert float(scale[i]) == pytest.approx((1 + i % 7) / 127, rel=1e-6)
+    assert int((scale != 1).sum()) == 5
+
+
 @pytest.mark.parametrize("bad", ["shape", "dtype", "columns", "host", "gain", "int"])
 def test_refusals(bad):
     x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")

@@ -134,6 +134,18 @@ def test_vocab_loss_refuses(bad, status):
                                                         a["ws_bytes"], stream=0)) == status
 
 
+def test_products_past_one_launch_are_refused():
+    # 2^24 tokens by 2^24 outputs: 2^32 tiles
+    assert _status(lambda: mo.poetx_linear_i8(1 << 24, 64, 1 << 24, BF, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 24,
+                                              stream=0)) == px.POETX_EUNSUPPORTED
+    D = mo.make_vocab(64, 1 << 24)
+    args = (D, 1 << 24, FAKE, 64, FAKE, 64, FAKE)
+    assert _status(lambda: mo.poetx_vocab_loss_forward(*args, FAKE, FAKE, FAKE, 1 << 62,
+                                                       stream=0)) == px.POETX_EUNSUPPORTED
+    assert _status(lambda: mo.poetx_vocab_loss_backward(*args, FAKE, None, 1.0, FAKE, FAKE, FAKE, 1 << 62,
+                                                        stream=0)) == px.POETX_EUNSUPPORTED
+
+
 def test_vocab_workspace_is_bounded_by_the_piece_not_the_logits():
     T, d, V = 8192, 4096, 131072
     bwd = mo.poetx_vocab_ws_bytes(mo.make_vocab(d, V), T, mo.POETX_OP_VOCAB_BACKWARD)
