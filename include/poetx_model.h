@@ -23,7 +23,7 @@
  *    exact); bfloat16 outputs are rounded once, to nearest even.
  *  - Results do not depend on the run: no output is summed by atomics.
  *  - Sizes within the limits below whose product makes more tiles than one
- *    launch holds (about 2^39 outputs), or w rows further apart than 2^22
+ *    launch holds (about 2^38 outputs), or w rows further apart than 2^22
  *    elements, give POETX_EUNSUPPORTED.
  */
 #ifndef POETX_MODEL_H

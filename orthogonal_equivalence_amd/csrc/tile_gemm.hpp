@@ -77,9 +77,9 @@ inline int pick_tile(const TileCost* tiles, int n, int64_t M, int64_t N, int ski
 }
 
 // A launch's threads in one dimension stay below 2^32: whether the chosen
-// tile's workgroups (of at most 512) do.
+// tile's workgroups (of at most 512, two products at most) do.
 inline bool tiles_fit(const TileCost& t, int64_t M, int64_t N) {
-  return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) < (int64_t(1) << 23);
+  return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn) < (int64_t(1) << 22);
 }
 
 // One operand: rows of K (K-contiguous), or rows of columns with K down.

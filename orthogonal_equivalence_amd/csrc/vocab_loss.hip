@@ -143,6 +143,7 @@ struct TileArgs {
   float* acc32;
   int first, last;
   void* out;
+  int tile;  // dw's of the wide ones
 };
 
 // storage of a tile's element size
@@ -155,12 +156,62 @@ struct Elem<4> {
   typedef float type;
 };
 
-// Tile index of the workgroup among the tiles of the counted rows; false past
-// them.
+// The tiles of 256 columns, one workgroup a CU, come in one kernel, which picks
+// among them.
+template <bool AKC, bool BKC, bool KTAIL>
+struct WideTiles {
+  typedef TileCfg<2, 128, 256, 2, 4, 3, AKC, BKC, KTAIL> T128;
+  typedef TileCfg<2, 256, 256, 2, 4, 2, AKC, BKC, KTAIL> T256;
+  // (192 rows do not divide into the whole-row loads of an operand with K as its rows)
+  typedef TileCfg<2, AKC ? 192 : 256, 256, 2, 4, 2, AKC, BKC, KTAIL> T192;
+  static constexpr int NT = 512, BN = 256;
+  static constexpr int LDS = T128::LDS > T256::LDS ? T128::LDS : T256::LDS;
+};
+template <class C>
+struct IsWide {
+  static constexpr bool value = false;
+};
+template <bool AKC, bool BKC, bool KTAIL>
+struct IsWide<WideTiles<AKC, BKC, KTAIL>> {
+  static constexpr bool value = true;
+};
+
+// the same tiles for dw's operands, which both have K as their rows
+template <class C>
+struct Turned;
+template <int ES, int BM, int BN, int WM, int WN, int NS, int KG>
+struct Turned<TileCfg<ES, BM, BN, WM, WN, NS, true, false, false, KG>> {
+  typedef TileCfg<ES, BM, BN, WM, WN, NS, false, false, false, KG> type;
+};
+template <>
+struct Turned<WideTiles<true, false, false>> {
+  typedef WideTiles<false, false, false> type;
+};
+
+// Which of them for the counted rows, whose number the host does not know: the
+// cheapest whose tiles fit the launch (T = 1111 of which 555 count, d = 2056, V
+// = 50021: forward 157 us with three rounds of 192 rows, 171 with three of 256).
+__device__ __forceinline__ int pick_wide(int rows, int tiles_n, int most) {
+  int best = kTile256;
+  float least = INFINITY;
+#pragma unroll
+  for (int k = kTile128x256; k <= kTile256; ++k) {
+    const int bm = kTileCosts[k].bm;
+    const int64_t n = static_cast<int64_t>((rows + bm - 1) / bm) * tiles_n;
+    const float us = static_cast<float>((n + 255) / 256) * static_cast<float>(kTileCosts[k].us);
+    if (n <= most && us < least) {
+      best = k;
+      least = us;
+    }
+  }
+  return best;
+}
+
+// Tile index of a workgroup, number bid, among the tiles of the counted rows;
+// false past them.
 template <int BM>
-__device__ __forceinline__ bool vocab_place(int count, int tiles_n, int& tm, int& tn) {
+__device__ __forceinline__ bool vocab_place(int bid, int count, int tiles_n, int& tm, int& tn) {
   const int tiles_m = (count + BM - 1) / BM;
-  const int bid = static_cast<int>(blockIdx.x);
   if (bid >= tiles_m * tiles_n) return false;
   tile_place(xcd_remap(bid, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   return true;
@@ -199,11 +250,9 @@ __device__ __forceinline__ void mask_columns(f32x4_t (&acc)[Cfg::TM][Cfg::TN], i
 // Maximum and sum of every row over the tile's columns, in powers of two, and
 // the targets' logits.
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[Cfg::LDS];
-  const int count = *a.r.count;
+__device__ __forceinline__ void stat_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
-  if (!vocab_place<Cfg::BM>(count, a.tiles_n, tm, tn)) return;
+  if (!vocab_place<Cfg::BM>(bid, count, a.tiles_n, tm, tn)) return;
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
@@ -255,6 +304,21 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_stat(const TileArgs a) {
   }
 }
 
+template <class C>
+__global__ void __launch_bounds__(C::NT, 1) k_vocab_stat(const TileArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int bid = blockIdx.x, count = *a.r.count;
+  if constexpr (IsWide<C>::value) {
+    switch (pick_wide(count, a.tiles_n, gridDim.x)) {
+      case kTile128x256: stat_tile<typename C::T128>(a, bid, count, smem); return;
+      case kTile192x256: stat_tile<typename C::T192>(a, bid, count, smem); return;
+      default: stat_tile<typename C::T256>(a, bid, count, smem); return;
+    }
+  } else {
+    stat_tile<C>(a, bid, count, smem);
+  }
+}
+
 // lse and loss of every token from the tiles' pairs: 64 tokens a workgroup,
 // 16 waves over every 16th tile.
 __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int tiles, const float* tl, const int32_t* pos,
@@ -287,11 +351,9 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
 // 0.17%). p [count][ldp], zero
 // in the columns past the vocabulary.
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[Cfg::LDS];
-  const int count = *a.r.count;
+__device__ __forceinline__ void dlogits_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
-  if (!vocab_place<Cfg::BM>(count, a.tiles_n, tm, tn)) return;
+  if (!vocab_place<Cfg::BM>(bid, count, a.tiles_n, tm, tn)) return;
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
@@ -324,14 +386,27 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dlogits(const TileArgs a) 
   });
 }
 
+template <class C>
+__global__ void __launch_bounds__(C::NT, 1) k_vocab_dlogits(const TileArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+  const int bid = blockIdx.x, count = *a.r.count;
+  if constexpr (IsWide<C>::value) {
+    switch (pick_wide(count, a.tiles_n, gridDim.x)) {
+      case kTile128x256: dlogits_tile<typename C::T128>(a, bid, count, smem); return;
+      case kTile192x256: dlogits_tile<typename C::T192>(a, bid, count, smem); return;
+      default: dlogits_tile<typename C::T256>(a, bid, count, smem); return;
+    }
+  } else {
+    dlogits_tile<C>(a, bid, count, smem);
+  }
+}
+
 // dh: the piece's product with its rows of w, added to the earlier pieces'
 // sums in float32; the last piece writes the tokens' rows.
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[Cfg::LDS];
-  const int count = *a.r.count;
+__device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
-  if (!vocab_place<Cfg::BM>(count, a.tiles_n, tm, tn)) return;
+  if (!vocab_place<Cfg::BM>(bid, count, a.tiles_n, tm, tn)) return;
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
@@ -362,11 +437,10 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dh(const TileArgs a) {
 
 // dw rows of a piece: the product over the counted tokens.
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int tiles_m) {
-  __shared__ __attribute__((aligned(1024))) char smem[Cfg::LDS];
-  const int count = *a.r.count;
+__device__ __forceinline__ void dw_tile(const TileArgs& a, int bid, int count, char* smem) {
+  const int tiles_m = (a.vn + Cfg::BM - 1) / Cfg::BM;
   int tm, tn;
-  tile_place(xcd_remap(blockIdx.x, gridDim.x), tiles_m, a.tiles_n, tm, tn);
+  tile_place(xcd_remap(bid, tiles_m * a.tiles_n), tiles_m, a.tiles_n, tm, tn);
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A, B = a.B;
   A.rows = count;
@@ -384,43 +458,83 @@ __global__ void __launch_bounds__(Cfg::NT, 1) k_vocab_dw(const TileArgs a, int t
   });
 }
 
+template <class CH>
+__device__ __forceinline__ void dh_part(const TileArgs& a, int bid, int nh, int count, char* smem) {
+  if constexpr (IsWide<CH>::value) {
+    switch (pick_wide(count, a.tiles_n, nh)) {
+      case kTile128x256: dh_tile<typename CH::T128>(a, bid, count, smem); return;
+      case kTile192x256: dh_tile<typename CH::T192>(a, bid, count, smem); return;
+      default: dh_tile<typename CH::T256>(a, bid, count, smem); return;
+    }
+  } else {
+    dh_tile<CH>(a, bid, count, smem);
+  }
+}
+template <class CW>
+__device__ __forceinline__ void dw_part(const TileArgs& a, int bid, int count, char* smem) {
+  if constexpr (IsWide<CW>::value) {
+    if (a.tile == kTile128x256) dw_tile<typename CW::T128>(a, bid, count, smem);
+    else dw_tile<typename CW::T256>(a, bid, count, smem);
+  } else {
+    dw_tile<CW>(a, bid, count, smem);
+  }
+}
+
+// dh and dw of a piece: dh's nh workgroups, then dw's, in one launch where both
+// take the same kind of tile, and else in two (NoTiles for the other's). One
+// launch is one latency and one tail: T = 256, d = 512, V = 1000 in float, loss
+// and gradients 40.6 us against 46.1.
+struct NoTiles {
+  static constexpr int NT = 0, LDS = 0;
+};
+template <class CH, class CW>
+__global__ void __launch_bounds__(CH::NT ? CH::NT : CW::NT, 1) k_vocab_grads(const TileArgs h, const TileArgs w, int nh) {
+  __shared__ __attribute__((aligned(1024))) char smem[CH::LDS > CW::LDS ? CH::LDS : CW::LDS];
+  const int bid = blockIdx.x, count = *h.r.count;
+  if constexpr (CH::NT != 0) {
+    if (CW::NT == 0 || bid < nh) {
+      dh_part<CH>(h, bid, nh, count, smem);
+      return;
+    }
+  }
+  if constexpr (CW::NT != 0) dw_part<CW>(w, bid - nh, count, smem);
+}
+
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 
-// (192 rows do not divide into the whole-row loads of an operand with K as its
-// rows, as dw's first one has)
 int pick(int64_t M, int64_t N, bool bf16, bool no_192 = false) {
   if (bf16) return pick_tile(kTileCosts, kTileKinds, M, N, no_192 ? kTile192x256 : -1);
   return pick_tile(kTileCostsF32, kTileKindsF32, M, N);
 }
+// workgroups of tile t over M x N
+int pick_count(int t, int64_t M, int64_t N, bool bf16) {
+  const TileCost& c = bf16 ? kTileCosts[t] : kTileCostsF32[t];
+  return tiles(M, c.bm) * tiles(N, c.bn);
+}
+// the kernel that has the tile: the wide ones share one
+int kernel_of(int t, bool bf16) { return bf16 && t > kTile128x256 ? kTile128x256 : t; }
 
-// f(config) for the element size and tile, K-contiguous operands or not
+// f(config) for the element size and kernel, K-contiguous operands or not
 template <bool AKC, bool BKC, bool KTAIL, class F>
-void with_tile(bool bf16, int t, F&& f) {
+void with_tile(bool bf16, int kernel, F&& f) {
   if (!bf16) {
-    switch (t) {
+    switch (kernel) {
       case kTileF32: f(TileCfg<4, 32, 32, 1, 1, 2, AKC, BKC, KTAIL, 8>{}); return;
       case kTileF64: f(TileCfg<4, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
       default: f(TileCfg<4, 128, 128, 2, 4, 3, AKC, BKC, KTAIL>{}); return;
     }
   }
-  switch (t) {
+  switch (kernel) {
     case kTile64x2: f(TileCfg<2, 64, 64, 2, 2, 3, AKC, BKC, KTAIL, 2>{}); return;
     case kTile64: f(TileCfg<2, 64, 64, 2, 2, 4, AKC, BKC, KTAIL>{}); return;
     case kTile128: f(TileCfg<2, 128, 128, 2, 4, 4, AKC, BKC, KTAIL>{}); return;
-    case kTile128x256: f(TileCfg<2, 128, 256, 2, 4, 3, AKC, BKC, KTAIL>{}); return;
-    case kTile192x256:
-      if constexpr (AKC) {
-        f(TileCfg<2, 192, 256, 2, 4, 2, AKC, BKC, KTAIL>{});
-        return;
-      }
-      [[fallthrough]];
-    default: f(TileCfg<2, 256, 256, 2, 4, 2, AKC, BKC, KTAIL>{}); return;
+    default: f(WideTiles<AKC, BKC, KTAIL>{}); return;
   }
 }
 template <class F>
-void with_logits_tile(bool bf16, int t, int64_t d, F&& f) {
-  if (d % (bf16 ? 64 : 32)) with_tile<true, true, true>(bf16, t, f);
-  else with_tile<true, true, false>(bf16, t, f);
+void with_logits_tile(bool bf16, int kernel, int64_t d, F&& f) {
+  if (d % (bf16 ? 64 : 32)) with_tile<true, true, true>(bf16, kernel, f);
+  else with_tile<true, true, false>(bf16, kernel, f);
 }
 
 void gather_rows(const VocabDesc& D, bool backward, hipStream_t st) {
@@ -464,10 +578,11 @@ void vocab_forward(const VocabDesc& D, hipStream_t st) {
   a.vn = static_cast<int>(D.V);
   a.stat = D.stat;
   a.tl = D.tl;
-  with_logits_tile(D.bf16, pick(D.T, D.V, D.bf16), D.d, [&](auto cfg) {
+  const int t = pick(D.T, D.V, D.bf16);
+  a.tiles_n = vocab_stat_tiles(D.T, D.V, D.bf16);
+  with_logits_tile(D.bf16, kernel_of(t, D.bf16), D.d, [&](auto cfg) {
     using C = decltype(cfg);
-    a.tiles_n = tiles(D.V, C::BN);
-    hipLaunchKernelGGL((k_vocab_stat<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+    hipLaunchKernelGGL((k_vocab_stat<C>), dim3(pick_count(t, D.T, D.V, D.bf16)), dim3(C::NT), 0, st, a);
   });
   hipLaunchKernelGGL(k_vocab_join, dim3(tiles(D.T, 64)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
                      D.loss, D.lse);
@@ -489,28 +604,40 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     a.acc32 = D.acc;
     a.A = {D.hc, D.ldhc, D.T, D.d};
     a.B = {w, D.ldw, vn, D.d};
-    with_logits_tile(D.bf16, pick(D.T, vn, D.bf16), D.d, [&](auto cfg) {
+    const int t = pick(D.T, vn, D.bf16);
+    with_logits_tile(D.bf16, kernel_of(t, D.bf16), D.d, [&](auto cfg) {
       using C = decltype(cfg);
       a.tiles_n = tiles(vn, C::BN);
-      hipLaunchKernelGGL((k_vocab_dlogits<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+      hipLaunchKernelGGL((k_vocab_dlogits<C>), dim3(pick_count(t, D.T, vn, D.bf16)), dim3(C::NT), 0, st, a);
     });
     // the columns of p up to the end of the last K step are zero, and so are
     // rows past an operand's end
     a.A = {D.p, D.piece, D.T, D.piece};
     a.out = D.dh;
-    with_tile<true, false, false>(D.bf16, pick(D.T, D.d, D.bf16), [&](auto cfg) {
-      using C = decltype(cfg);
-      a.tiles_n = tiles(D.d, C::BN);
-      hipLaunchKernelGGL((k_vocab_dh<C>), dim3(static_cast<unsigned>(tiles(T, C::BM)) * a.tiles_n), dim3(C::NT), 0, st, a);
+    TileArgs b = a;
+    b.B = {D.hc, D.ldhc, D.T, D.d};
+    b.out = D.dw;
+    const int th = pick(D.T, D.d, D.bf16), tw = pick(vn, D.d, D.bf16, true);
+    const int nh = pick_count(th, D.T, D.d, D.bf16), nw = pick_count(tw, vn, D.d, D.bf16);
+    b.tile = tw;
+    const int kh = kernel_of(th, D.bf16), kw = kernel_of(tw, D.bf16);
+    with_tile<true, false, false>(D.bf16, kh, [&](auto cfg) {
+      using CH = decltype(cfg);
+      a.tiles_n = tiles(D.d, CH::BN);
+      if (kh == kw) {
+        b.tiles_n = a.tiles_n;
+        typedef typename Turned<CH>::type CW;
+        hipLaunchKernelGGL((k_vocab_grads<CH, CW>), dim3(nh + nw), dim3(CH::NT), 0, st, a, b, nh);
+      } else {
+        hipLaunchKernelGGL((k_vocab_grads<CH, NoTiles>), dim3(nh), dim3(CH::NT), 0, st, a, b, nh);
+      }
     });
-    a.B = {D.hc, D.ldhc, D.T, D.d};
-    a.out = D.dw;
-    with_tile<false, false, false>(D.bf16, pick(vn, D.d, D.bf16, true), [&](auto cfg) {
-      using C = decltype(cfg);
-      a.tiles_n = tiles(D.d, C::BN);
-      const int tm = tiles(vn, C::BM);
-      hipLaunchKernelGGL((k_vocab_dw<C>), dim3(static_cast<unsigned>(tm) * a.tiles_n), dim3(C::NT), 0, st, a, tm);
-    });
+    if (kh != kw)
+      with_tile<false, false, false>(D.bf16, kw, [&](auto cfg) {
+        using CW = decltype(cfg);
+        b.tiles_n = tiles(D.d, CW::BN);
+        hipLaunchKernelGGL((k_vocab_grads<NoTiles, CW>), dim3(nw), dim3(CW::NT), 0, st, a, b, 0);
+      });
   }
 }
 

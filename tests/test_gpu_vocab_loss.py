@@ -76,6 +76,26 @@ def test_loss_and_gradients(T, d, V, act):
     _check(h, w, _targets(rng, T, V, 0.3 if T > 1 else 0.0), act)
 
 
+# Sizes that take the widest tiles, forward (V) or backward (d), with fewer and
+# fewer counted tokens: the tile goes by their number, which the launch does not
+# know.
+@pytest.mark.parametrize("ignored", [0.0, 0.3, 0.6, 0.97])
+@pytest.mark.parametrize("T,d,V", [(1111, 72, 20021), (1000, 64, 16384), (1500, 2056, 2300), (2500, 2504, 2490)])
+def test_wide_tiles_by_the_counted_tokens(T, d, V, ignored):
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V} ignored={ignored}", flush=True)
+    rng = np.random.default_rng([T, int(100 * ignored)])
+    h, w = normal(rng, (T, d), "bf16"), normal(rng, (V, d), "bf16", 2.0 / np.sqrt(d))
+    _check(h, w, _targets(rng, T, V, ignored), "bf16")
+
+
+def test_the_largest_tiles():
+    T, d, V = 4000, 4096, 4000
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V}", flush=True)
+    rng = np.random.default_rng(T)
+    h, w = normal(rng, (T, d), "bf16"), normal(rng, (V, d), "bf16", 2.0 / np.sqrt(d))
+    _check(h, w, _targets(rng, T, V, 0.05), "bf16")
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("piece", [1, 256, 300, 512, 100000])
 def test_pieces(piece, act):
