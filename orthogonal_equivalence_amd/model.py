@@ -138,6 +138,7 @@ def rms_norm_backward(dy, h, rstd, gain, dh=None):
     dy = _grad(dy)
     (T, n), dev, dt = _first("dy", dy)
     lddy = _rows("dy", dy, dy.shape, dy.dtype, dev)
+    h = h if h.is_contiguous() else h.contiguous()  # without a residual h is the caller's x, of any row stride
     _flat("h", h, dy.shape, dy.dtype, dev)
     _flat("rstd", rstd, (T,), torch.float32, dev)
     _flat("gain", gain, (n,), torch.float32, dev)

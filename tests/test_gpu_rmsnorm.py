@@ -96,6 +96,17 @@ def test_no_residual_and_the_stream_itself():
     within("dx", dx, DX, U16 * np.abs(DX) + 1e-5)
 
 
+def test_strided_stream_without_a_residual():
+    rng = np.random.default_rng(8)
+    x, gain, dy = strided(normal(rng, (9, 640), "bf16"), 8), normal(rng, 640, "f32"), normal(rng, (9, 640), "bf16")
+    h, y, rstd = model.rms_norm(x, gain)
+    assert h is x
+    got = model.rms_norm_backward(dy, h, rstd, gain)
+    want = model.rms_norm_backward(dy, x.contiguous(), rstd, gain)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("n", [256, 4096, 40000])
 def test_in_place_and_strided(n):
     print(f"\n[gpu] rms_norm in place, strided n={n}", flush=True)

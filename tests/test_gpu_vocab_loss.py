@@ -88,6 +88,17 @@ def test_wide_tiles_by_the_counted_tokens(T, d, V, ignored):
     _check(h, w, _targets(rng, T, V, ignored), "bf16")
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2047, 2049, 16385, 70000])
+def test_many_tokens(T, act):
+    """Tokens past one round of the gather, in workgroups of 4, 16 and 64 or more."""
+    print(f"\n[gpu] vocab_loss T={T} {act}", flush=True)
+    rng = np.random.default_rng(T)
+    d, V = 72, 40
+    h, w = normal(rng, (T, d), act), normal(rng, (V, d), act, 0.2)
+    _check(h, w, _targets(rng, T, V, 0.4), act, normal(rng, T, "f32"))
+
+
 def test_the_largest_tiles():
     T, d, V = 4000, 4096, 4000
     print(f"\n[gpu] vocab_loss T={T} d={d} V={V}", flush=True)
