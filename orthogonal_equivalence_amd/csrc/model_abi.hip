@@ -99,7 +99,8 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.hc = c.take<char>(T * v.ldhc * es);
   if (bwd) {
     v.p = c.take<char>(T * v.piece * es);
-    if (v.piece < D->V) v.acc = c.take<float>(T * D->d);
+    v.dh_plan = vocab_dh_plan(std::max<int64_t>(T, 1), D->d, std::min(v.piece, D->V), bf);
+    if (v.piece < D->V || v.dh_plan.splits > 1) v.acc = c.take<float>(v.dh_plan.splits * T * D->d);
     return;
   }
   v.tl = c.take<float>(T);

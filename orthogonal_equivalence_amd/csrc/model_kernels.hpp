@@ -71,6 +71,11 @@ struct VocabRows {
   float* lse;      // [T] lse of compact row c (backward)
   int32_t* count;  // [1] counted tokens
 };
+// Tile of dh's product, and the sets of workgroups that its K is split over.
+struct DhPlan {
+  int tile = 0, splits = 1;
+};
+DhPlan vocab_dh_plan(int64_t T, int64_t d, int64_t piece, bool bf16);
 struct VocabDesc {
   const void* h = nullptr;
   int64_t ldh = 0;
@@ -93,7 +98,8 @@ struct VocabDesc {
   float scale = 1.f;
   void* p = nullptr;        // [T][piece] gradient of a piece's logits
   int64_t piece = 0;        // a multiple of 256
-  float* acc = nullptr;     // [T][d] sum of dh over the pieces (more than one)
+  DhPlan dh_plan;
+  float* acc = nullptr;     // [splits][T][d] sums of dh (more than one split or piece)
   void* dh = nullptr;
   void* dw = nullptr;
 };

@@ -150,8 +150,9 @@ struct TileArgs {
   // dh, dw
   float* acc32;
   int first, last;
+  int splits;      // of dh's K over workgroups
   void* out;
-  int tile;  // dw's of the wide ones
+  int tile;        // of the wide ones: dw's, and dh's where it is split
 };
 
 // storage of a tile's element size
@@ -327,24 +328,29 @@ __global__ void __launch_bounds__(C::NT, 1) k_vocab_stat(const TileArgs a) {
   }
 }
 
-// lse and loss of every token from the tiles' pairs: 64 tokens a workgroup,
-// 16 waves over every 16th tile.
+// lse and loss of every token from the tiles' pairs: N tokens a workgroup, 1024
+// / N threads a token over the tiles. Bound by latencies: 8 tokens (a row's
+// pairs of one 64-byte piece) where there are tiles for their threads, else 64
+// (T = 16, 2048 tiles: 8 us, 64 tokens 25; T = 40000, one tile: 22 us and 5).
+template <int N>
 __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int tiles, const float* tl, const int32_t* pos,
                                                      int T, float* loss, float* lse) {
-  __shared__ float2 red[16][64];
+  __shared__ float2 red[16][N];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 64 + lane;
+  const int t = blockIdx.x * N + lane % N;
   const int c = t < T ? pos[t] : -1;
   float m = -INFINITY, s = 0.f;
   if (c >= 0)
 #pragma unroll 4
-    for (int k = wave; k < tiles; k += 16) {
+    for (int k = threadIdx.x / N; k < tiles; k += 1024 / N) {
       const float2 v = stat[static_cast<int64_t>(k) * T + c];
       join_stat(m, s, v.x, v.y);
     }
-  red[wave][lane] = make_float2(m, s);
+#pragma unroll
+  for (int o = N; o < 64; o <<= 1) join_stat(m, s, __shfl_xor(m, o), __shfl_xor(s, o));
+  if (lane < N) red[wave][lane] = make_float2(m, s);
   __syncthreads();
-  if (wave || t >= T) return;
+  if (threadIdx.x >= N || t >= T) return;
 #pragma unroll
   for (int w = 1; w < 16; ++w) join_stat(m, s, red[w][lane].x, red[w][lane].y);
   const float l = c >= 0 ? (m + __builtin_amdgcn_logf(s)) * kLn2 : 0.f;
@@ -410,22 +416,27 @@ __global__ void __launch_bounds__(C::NT, 1) k_vocab_dlogits(const TileArgs a) {
 }
 
 // dh: the piece's product with its rows of w, added to the earlier pieces'
-// sums in float32; the last piece writes the tokens' rows.
+// sums in float32; the last piece writes the tokens' rows. Where the tiles of
+// few tokens leave CUs idle, the piece's rows are split over `splits` sets of
+// workgroups with sums of their own, which k_vocab_dh_join adds up.
 template <class Cfg>
-__device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int count, char* smem) {
+__device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int nh, int count, char* smem) {
+  const int tiles_h = nh / a.splits, split = bid / tiles_h;
   int tm, tn;
-  if (!vocab_place<Cfg::BM>(bid, count, a.tiles_n, tm, tn)) return;
+  if (!vocab_place<Cfg::BM>(bid % tiles_h, count, a.tiles_n, tm, tn)) return;
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A;
   A.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, a.B, m0, n0, 0, (a.vn + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  const int steps = (a.vn + Cfg::BK - 1) / Cfg::BK, per = (steps + a.splits - 1) / a.splits;
+  tile_product<Cfg>(A, a.B, m0, n0, split * per, min(steps, (split + 1) * per), smem, acc);
   const float unit = *a.r.unit;
+  float* const sums = a.acc32 + static_cast<int64_t>(split) * a.T * a.d;
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int c = m0 + row, k = n0 + col;
     if (c >= count || k >= a.d) return;
     float o[8];
-    float* sum = a.acc32 + static_cast<int64_t>(c) * a.d + k;
+    float* sum = sums + static_cast<int64_t>(c) * a.d + k;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = v[i];
     if (!a.first) {
@@ -433,7 +444,7 @@ __device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int count, c
       o[0] += s0.x; o[1] += s0.y; o[2] += s0.z; o[3] += s0.w;
       o[4] += s1.x; o[5] += s1.y; o[6] += s1.z; o[7] += s1.w;
     }
-    if (a.last) {
+    if (a.last && a.splits == 1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] *= unit;
       tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
@@ -441,6 +452,28 @@ __device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int count, c
       tile_store8(sum, o);
     }
   });
+}
+
+// The counted tokens' rows of dh from the splits' sums, 8 features a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_dh_join(const TileArgs a) {
+  const int chunks = a.d / 8;
+  const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  const int64_t c = i / chunks;
+  if (c >= *a.r.count) return;
+  const int k = static_cast<int>(i % chunks) * 8;
+  float o[8] = {};
+  const float* sum = a.acc32 + c * a.d + k;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s, sum += static_cast<int64_t>(a.T) * a.d) {
+    const float4 s0 = *reinterpret_cast<const float4*>(sum), s1 = *reinterpret_cast<const float4*>(sum + 4);
+    o[0] += s0.x; o[1] += s0.y; o[2] += s0.z; o[3] += s0.w;
+    o[4] += s1.x; o[5] += s1.y; o[6] += s1.z; o[7] += s1.w;
+  }
+  const float unit = *a.r.unit;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] *= unit;
+  tile_store8(static_cast<T*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
 }
 
 // dw rows of a piece: the product over the counted tokens.
@@ -469,13 +502,13 @@ __device__ __forceinline__ void dw_tile(const TileArgs& a, int bid, int count, c
 template <class CH>
 __device__ __forceinline__ void dh_part(const TileArgs& a, int bid, int nh, int count, char* smem) {
   if constexpr (IsWide<CH>::value) {
-    switch (pick_wide(count, a.tiles_n, nh)) {
-      case kTile128x256: dh_tile<typename CH::T128>(a, bid, count, smem); return;
-      case kTile192x256: dh_tile<typename CH::T192>(a, bid, count, smem); return;
-      default: dh_tile<typename CH::T256>(a, bid, count, smem); return;
+    switch (a.splits == 1 ? pick_wide(count, a.tiles_n, nh) : a.tile) {
+      case kTile128x256: dh_tile<typename CH::T128>(a, bid, nh, count, smem); return;
+      case kTile192x256: dh_tile<typename CH::T192>(a, bid, nh, count, smem); return;
+      default: dh_tile<typename CH::T256>(a, bid, nh, count, smem); return;
     }
   } else {
-    dh_tile<CH>(a, bid, count, smem);
+    dh_tile<CH>(a, bid, nh, count, smem);
   }
 }
 template <class CW>
@@ -570,12 +603,38 @@ TileArgs tile_args(const VocabDesc& D) {
 
 }  // namespace
 
+DhPlan vocab_dh_plan(int64_t T, int64_t d, int64_t piece, bool bf16) {
+  // Tile and splits together: rounds of workgroups, each of steps / splits
+  // K steps, and the sums' bytes (d = 4096, V = 131072: dh of 16 tokens 225 us, 580
+  // unsplit; backward of 600 tokens 2.13 ms, 2.70; d = 1024, V = 32000, 64 tokens:
+  // backward 67 us, 171).
+  const TileCost* costs = bf16 ? kTileCosts : kTileCostsF32;
+  const int64_t steps = (piece + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
+  DhPlan best{};
+  double least = 0;
+  for (int t = 0; t < (bf16 ? static_cast<int>(kTileKinds) : static_cast<int>(kTileKindsF32)); ++t) {
+    const int64_t n = static_cast<int64_t>(tiles(T, costs[t].bm)) * tiles(d, costs[t].bn);
+    for (int s = 1; s <= 16 && (s == 1 || steps / s >= 8); ++s) {
+      const double step = costs[t].us / (bf16 ? 32 : 1);
+      double us = static_cast<double>((n * s + costs[t].slots - 1) / costs[t].slots) * static_cast<double>((steps + s - 1) / s) * step;
+      if (s > 1) us += 4.0 + static_cast<double>(T) * static_cast<double>(d) * 8.0 * s / 4e6;
+      if (t == 0 && s == 1 || us < least) {
+        least = us;
+        best.tile = t;
+        best.splits = s;
+      }
+    }
+  }
+  return best;
+}
+
 bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
   const TileCost* t = bf16 ? kTileCosts : kTileCostsF32;
   const int64_t last = V % piece ? V % piece : piece;
   for (int64_t vn : {std::min(V, piece), last})
     if (!tiles_fit(t[pick(T, vn, bf16)], T, vn) || !tiles_fit(t[pick(vn, d, bf16, true)], vn, d)) return false;
-  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[pick(T, d, bf16)], T, d);
+  const DhPlan h = vocab_dh_plan(T, d, std::min(piece, V), bf16);
+  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[h.tile], T, d * h.splits);
 }
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
@@ -598,8 +657,12 @@ void vocab_forward(const VocabDesc& D, hipStream_t st) {
     using C = decltype(cfg);
     hipLaunchKernelGGL((k_vocab_stat<C>), dim3(pick_count(t, D.T, D.V, D.bf16)), dim3(C::NT), 0, st, a);
   });
-  hipLaunchKernelGGL(k_vocab_join, dim3(tiles(D.T, 64)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
-                     D.loss, D.lse);
+  auto join = [&](auto kernel, int tokens) {
+    hipLaunchKernelGGL(kernel, dim3(tiles(D.T, tokens)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
+                       D.loss, D.lse);
+  };
+  if (a.tiles_n >= 128) join(k_vocab_join<8>, 8);
+  else join(k_vocab_join<64>, 64);
 }
 
 void vocab_backward(const VocabDesc& D, hipStream_t st) {
@@ -616,6 +679,7 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     a.p = D.p;
     a.ldp = D.piece;
     a.acc32 = D.acc;
+    a.splits = D.dh_plan.splits;
     a.A = {D.hc, D.ldhc, D.T, D.d};
     a.B = {w, D.ldw, vn, D.d};
     const int t = pick(D.T, vn, D.bf16);
@@ -631,8 +695,9 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     TileArgs b = a;
     b.B = {D.hc, D.ldhc, D.T, D.d};
     b.out = D.dw;
-    const int th = pick(D.T, D.d, D.bf16), tw = pick(vn, D.d, D.bf16, true);
-    const int nh = pick_count(th, D.T, D.d, D.bf16), nw = pick_count(tw, vn, D.d, D.bf16);
+    const int th = D.dh_plan.tile, tw = pick(vn, D.d, D.bf16, true);
+    const int nh = pick_count(th, D.T, D.d, D.bf16) * D.dh_plan.splits, nw = pick_count(tw, vn, D.d, D.bf16);
+    a.tile = th;
     b.tile = tw;
     const int kh = kernel_of(th, D.bf16), kw = kernel_of(tw, D.bf16);
     with_tile<true, false, false>(D.bf16, kh, [&](auto cfg) {
@@ -652,6 +717,12 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
         b.tiles_n = tiles(D.d, CW::BN);
         hipLaunchKernelGGL((k_vocab_grads<NoTiles, CW>), dim3(nw), dim3(CW::NT), 0, st, a, b, 0);
       });
+    if (a.last && a.splits > 1) {
+      const int n = tiles(D.T * (D.d / 8), 256), most = 1 << 20;
+      const dim3 grid(std::min(n, most), tiles(n, most));
+      if (D.bf16) hipLaunchKernelGGL(k_vocab_dh_join<bf16_t>, grid, dim3(256), 0, st, a);
+      else hipLaunchKernelGGL(k_vocab_dh_join<float>, grid, dim3(256), 0, st, a);
+    }
   }
 }
 

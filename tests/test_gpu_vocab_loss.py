@@ -99,6 +99,17 @@ def test_many_tokens(T, act):
     _check(h, w, _targets(rng, T, V, 0.4), act, normal(rng, T, "f32"))
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,piece", [(1, 64, 20000, 0), (16, 520, 16391, 0), (70, 72, 30000, 4096),
+                                         (130, 264, 9000, 8192), (300, 1032, 12001, 0)])
+def test_few_tokens_and_a_long_vocabulary(T, d, V, piece, act):
+    """dh's sum over the vocabulary split over workgroups, pieces or not."""
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V} piece={piece} {act}", flush=True)
+    rng = np.random.default_rng([T, V])
+    h, w = normal(rng, (T, d), act), normal(rng, (V, d), act, 2.0 / np.sqrt(d))
+    _check(h, w, _targets(rng, T, V, 0.2 if T > 1 else 0.0), act, piece=piece)
+
+
 def test_the_largest_tiles():
     T, d, V = 4000, 4096, 4000
     print(f"\n[gpu] vocab_loss T={T} d={d} V={V}", flush=True)
