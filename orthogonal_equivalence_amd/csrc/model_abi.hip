@@ -99,8 +99,11 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.hc = c.take<char>(T * v.ldhc * es);
   if (bwd) {
     v.p = c.take<char>(T * v.piece * es);
-    v.dh_plan = vocab_dh_plan(std::max<int64_t>(T, 1), D->d, std::min(v.piece, D->V), bf);
+    const int64_t t = std::max<int64_t>(T, 1), rows = std::min(v.piece, D->V);
+    v.dh_plan = vocab_dh_plan(t, D->d, D->V, v.piece, bf);
+    v.dw_plan = vocab_dw_plan(t, D->d, D->V, v.piece, bf);
     if (v.piece < D->V || v.dh_plan.splits > 1) v.acc = c.take<float>(v.dh_plan.splits * T * D->d);
+    if (v.dw_plan.splits > 1) v.acc_w = c.take<float>(v.dw_plan.splits * rows * D->d);
     return;
   }
   v.tl = c.take<float>(T);

@@ -71,11 +71,12 @@ struct VocabRows {
   float* lse;      // [T] lse of compact row c (backward)
   int32_t* count;  // [1] counted tokens
 };
-// Tile of dh's product, and the sets of workgroups that its K is split over.
-struct DhPlan {
+// Tile of dh's or dw's product, and the sets of workgroups that its K is split over.
+struct KPlan {
   int tile = 0, splits = 1;
 };
-DhPlan vocab_dh_plan(int64_t T, int64_t d, int64_t piece, bool bf16);
+KPlan vocab_dh_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
+KPlan vocab_dw_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
 struct VocabDesc {
   const void* h = nullptr;
   int64_t ldh = 0;
@@ -98,8 +99,9 @@ struct VocabDesc {
   float scale = 1.f;
   void* p = nullptr;        // [T][piece] gradient of a piece's logits
   int64_t piece = 0;        // a multiple of 256
-  DhPlan dh_plan;
+  KPlan dh_plan, dw_plan;
   float* acc = nullptr;     // [splits][T][d] sums of dh (more than one split or piece)
+  float* acc_w = nullptr;   // [splits][piece][d] sums of a piece of dw (more than one split)
   void* dh = nullptr;
   void* dw = nullptr;
 };

@@ -59,12 +59,11 @@ constexpr TileCost kTileCosts[kTileKinds] = {{64, 64, 256, 11.2},   {64, 64, 512
 enum TileKindF32 { kTileF32, kTileF64, kTileF128, kTileKindsF32 };
 constexpr TileCost kTileCostsF32[kTileKindsF32] = {{32, 32, 256, 0.17}, {64, 64, 256, 0.60}, {128, 128, 256, 2.03}};
 
-// index of the cheapest of n tiles for an M x N product, without tile `skip`
-inline int pick_tile(const TileCost* tiles, int n, int64_t M, int64_t N, int skip = -1) {
+// index of the cheapest of n tiles for an M x N product
+inline int pick_tile(const TileCost* tiles, int n, int64_t M, int64_t N) {
   int best = -1;
   double least = 0;
   for (int i = 0; i < n; ++i) {
-    if (i == skip) continue;
     const TileCost& t = tiles[i];
     const int64_t count = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
     const double us = static_cast<double>((count + t.slots - 1) / t.slots) * t.us;

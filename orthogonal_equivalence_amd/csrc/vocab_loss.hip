@@ -150,7 +150,7 @@ struct TileArgs {
   // dh, dw
   float* acc32;
   int first, last;
-  int splits;      // of dh's K over workgroups
+  int splits;      // of K over workgroups
   void* out;
   int tile;        // of the wide ones: dw's, and dh's where it is split
 };
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_vocab_dlogits(const TileArgs a) {
 // dh: the piece's product with its rows of w, added to the earlier pieces'
 // sums in float32; the last piece writes the tokens' rows. Where the tiles of
 // few tokens leave CUs idle, the piece's rows are split over `splits` sets of
-// workgroups with sums of their own, which k_vocab_dh_join adds up.
+// workgroups with sums of their own, which k_vocab_join_splits adds up.
 template <class Cfg>
 __device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int nh, int count, char* smem) {
   const int tiles_h = nh / a.splits, split = bid / tiles_h;
@@ -454,18 +454,19 @@ __device__ __forceinline__ void dh_tile(const TileArgs& a, int bid, int nh, int 
   });
 }
 
-// The counted tokens' rows of dh from the splits' sums, 8 features a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) k_vocab_dh_join(const TileArgs a) {
+// Rows of dh (the counted tokens') or of a piece of dw from the splits' sums, 8
+// features a thread. `rows`: of one split's sums.
+template <typename T, bool DH>
+__global__ void __launch_bounds__(256) k_vocab_join_splits(const TileArgs a, int rows) {
   const int chunks = a.d / 8;
   const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t c = i / chunks;
-  if (c >= *a.r.count) return;
+  if (c >= (DH ? *a.r.count : rows)) return;
   const int k = static_cast<int>(i % chunks) * 8;
   float o[8] = {};
   const float* sum = a.acc32 + c * a.d + k;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s, sum += static_cast<int64_t>(a.T) * a.d) {
+  for (int s = 0; s < a.splits; ++s, sum += static_cast<int64_t>(rows) * a.d) {
     const float4 s0 = *reinterpret_cast<const float4*>(sum), s1 = *reinterpret_cast<const float4*>(sum + 4);
     o[0] += s0.x; o[1] += s0.y; o[2] += s0.z; o[3] += s0.w;
     o[4] += s1.x; o[5] += s1.y; o[6] += s1.z; o[7] += s1.w;
@@ -473,25 +474,32 @@ __global__ void __launch_bounds__(256) k_vocab_dh_join(const TileArgs a) {
   const float unit = *a.r.unit;
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] *= unit;
-  tile_store8(static_cast<T*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
+  tile_store8(static_cast<T*>(a.out) + (DH ? static_cast<int64_t>(a.r.idx[c]) : a.v0 + c) * a.d + k, o);
 }
 
-// dw rows of a piece: the product over the counted tokens.
+// dw rows of a piece: the product over the counted tokens, split over sets of
+// workgroups where the tiles of a small vocabulary leave CUs idle.
 template <class Cfg>
 __device__ __forceinline__ void dw_tile(const TileArgs& a, int bid, int count, char* smem) {
-  const int tiles_m = (a.vn + Cfg::BM - 1) / Cfg::BM;
+  const int tiles_m = (a.vn + Cfg::BM - 1) / Cfg::BM, tiles_w = tiles_m * a.tiles_n, split = bid / tiles_w;
   int tm, tn;
-  tile_place(xcd_remap(bid, tiles_m * a.tiles_n), tiles_m, a.tiles_n, tm, tn);
+  tile_place(xcd_remap(bid % tiles_w, tiles_w), tiles_m, a.tiles_n, tm, tn);
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   TileOperand A = a.A, B = a.B;
   A.rows = count;
   B.rows = count;
   f32x4_t acc[Cfg::TM][Cfg::TN];
-  tile_product<Cfg>(A, B, m0, n0, 0, (count + Cfg::BK - 1) / Cfg::BK, smem, acc);
+  const int steps = (count + Cfg::BK - 1) / Cfg::BK, per = (steps + a.splits - 1) / a.splits;
+  tile_product<Cfg>(A, B, m0, n0, split * per, min(steps, (split + 1) * per), smem, acc);
   const float unit = *a.r.unit;
+  float* const sums = a.acc32 + static_cast<int64_t>(split) * a.vn * a.d;
   tile_rows<Cfg>(acc, smem, [&](int row, int col, const float(&v)[8]) {
     const int m = m0 + row, k = n0 + col;
     if (m >= a.vn || k >= a.d) return;
+    if (a.splits > 1) {
+      tile_store8(sums + static_cast<int64_t>(m) * a.d + k, v);
+      return;
+    }
     float o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = v[i] * unit;
@@ -543,8 +551,8 @@ __global__ void __launch_bounds__(CH::NT ? CH::NT : CW::NT, 1) k_vocab_grads(con
 
 int tiles(int64_t n, int b) { return static_cast<int>((n + b - 1) / b); }
 
-int pick(int64_t M, int64_t N, bool bf16, bool no_192 = false) {
-  if (bf16) return pick_tile(kTileCosts, kTileKinds, M, N, no_192 ? kTile192x256 : -1);
+int pick(int64_t M, int64_t N, bool bf16) {
+  if (bf16) return pick_tile(kTileCosts, kTileKinds, M, N);
   return pick_tile(kTileCostsF32, kTileKindsF32, M, N);
 }
 // workgroups of tile t over M x N
@@ -603,22 +611,25 @@ TileArgs tile_args(const VocabDesc& D) {
 
 }  // namespace
 
-DhPlan vocab_dh_plan(int64_t T, int64_t d, int64_t piece, bool bf16) {
+KPlan vocab_k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
   // Tile and splits together: rounds of workgroups, each of steps / splits
   // K steps, and the sums' bytes (d = 4096, V = 131072: dh of 16 tokens 225 us, 580
   // unsplit; backward of 600 tokens 2.13 ms, 2.70; d = 1024, V = 32000, 64 tokens:
   // backward 67 us, 171).
   const TileCost* costs = bf16 ? kTileCosts : kTileCostsF32;
-  const int64_t steps = (piece + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
-  DhPlan best{};
-  double least = 0;
-  for (int t = 0; t < (bf16 ? static_cast<int>(kTileKinds) : static_cast<int>(kTileKindsF32)); ++t) {
-    const int64_t n = static_cast<int64_t>(tiles(T, costs[t].bm)) * tiles(d, costs[t].bn);
+  const int kinds = bf16 ? static_cast<int>(kTileKinds) : static_cast<int>(kTileKindsF32);
+  const int64_t steps = (K + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
+  KPlan best{};
+  double least = INFINITY;
+  for (int t = 0; t < kinds; ++t) {
+    if (bf16 && no_192 && t == kTile192x256) continue;
+    const int64_t n = ((M + costs[t].bm - 1) / costs[t].bm) * ((N + costs[t].bn - 1) / costs[t].bn);
+    const double step = costs[t].us / (bf16 ? 32 : 1);
     for (int s = 1; s <= 16 && (s == 1 || steps / s >= 8); ++s) {
-      const double step = costs[t].us / (bf16 ? 32 : 1);
-      double us = static_cast<double>((n * s + costs[t].slots - 1) / costs[t].slots) * static_cast<double>((steps + s - 1) / s) * step;
-      if (s > 1) us += 4.0 + static_cast<double>(T) * static_cast<double>(d) * 8.0 * s / 4e6;
-      if (t == 0 && s == 1 || us < least) {
+      double us = static_cast<double>((n * s + costs[t].slots - 1) / costs[t].slots) *
+                  static_cast<double>((steps + s - 1) / s) * step;
+      if (s > 1) us += 4.0 + static_cast<double>(M) * static_cast<double>(N) * 8.0 * s / 4e6;
+      if (us < least) {
         least = us;
         best.tile = t;
         best.splits = s;
@@ -627,14 +638,20 @@ DhPlan vocab_dh_plan(int64_t T, int64_t d, int64_t piece, bool bf16) {
   }
   return best;
 }
+KPlan vocab_dh_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
+  return vocab_k_plan(T, d, std::min(piece, V), bf16, false);
+}
+KPlan vocab_dw_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
+  return vocab_k_plan(std::min(piece, V), d, T, bf16, true);
+}
 
 bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
   const TileCost* t = bf16 ? kTileCosts : kTileCostsF32;
-  const int64_t last = V % piece ? V % piece : piece;
-  for (int64_t vn : {std::min(V, piece), last})
-    if (!tiles_fit(t[pick(T, vn, bf16)], T, vn) || !tiles_fit(t[pick(vn, d, bf16, true)], vn, d)) return false;
-  const DhPlan h = vocab_dh_plan(T, d, std::min(piece, V), bf16);
-  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[h.tile], T, d * h.splits);
+  const int64_t most = std::min(V, piece), last = V % piece ? V % piece : piece;
+  const KPlan h = vocab_dh_plan(T, d, V, piece, bf16), w = vocab_dw_plan(T, d, V, piece, bf16);
+  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[pick(T, most, bf16)], T, most) &&
+         tiles_fit(t[pick(T, last, bf16)], T, last) && tiles_fit(t[h.tile], T, d * h.splits) &&
+         tiles_fit(t[w.tile], most, d * w.splits);
 }
 
 int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
@@ -695,8 +712,10 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
     TileArgs b = a;
     b.B = {D.hc, D.ldhc, D.T, D.d};
     b.out = D.dw;
-    const int th = D.dh_plan.tile, tw = pick(vn, D.d, D.bf16, true);
-    const int nh = pick_count(th, D.T, D.d, D.bf16) * D.dh_plan.splits, nw = pick_count(tw, vn, D.d, D.bf16);
+    b.acc32 = D.acc_w;
+    b.splits = D.dw_plan.splits;
+    const int th = D.dh_plan.tile, tw = D.dw_plan.tile;
+    const int nh = pick_count(th, D.T, D.d, D.bf16) * a.splits, nw = pick_count(tw, vn, D.d, D.bf16) * b.splits;
     a.tile = th;
     b.tile = tw;
     const int kh = kernel_of(th, D.bf16), kw = kernel_of(tw, D.bf16);
@@ -717,12 +736,13 @@ void vocab_backward(const VocabDesc& D, hipStream_t st) {
         b.tiles_n = tiles(D.d, CW::BN);
         hipLaunchKernelGGL((k_vocab_grads<NoTiles, CW>), dim3(nw), dim3(CW::NT), 0, st, a, b, 0);
       });
-    if (a.last && a.splits > 1) {
-      const int n = tiles(D.T * (D.d / 8), 256), most = 1 << 20;
-      const dim3 grid(std::min(n, most), tiles(n, most));
-      if (D.bf16) hipLaunchKernelGGL(k_vocab_dh_join<bf16_t>, grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL(k_vocab_dh_join<float>, grid, dim3(256), 0, st, a);
-    }
+    auto join = [&](auto kernel, const TileArgs& args, int64_t rows) {
+      const int64_t n = (rows * (D.d / 8) + 255) / 256, most = 1 << 20;
+      hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(std::min(n, most)), tiles(n, 1 << 20)), dim3(256), 0, st,
+                         args, static_cast<int>(rows));
+    };
+    if (a.last && a.splits > 1) D.bf16 ? join(k_vocab_join_splits<bf16_t, true>, a, D.T) : join(k_vocab_join_splits<float, true>, a, D.T);
+    if (b.splits > 1) D.bf16 ? join(k_vocab_join_splits<bf16_t, false>, b, vn) : join(k_vocab_join_splits<float, false>, b, vn);
   }
 }
 

@@ -110,6 +110,16 @@ def test_few_tokens_and_a_long_vocabulary(T, d, V, piece, act):
     _check(h, w, _targets(rng, T, V, 0.2 if T > 1 else 0.0), act, piece=piece)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,piece", [(9000, 520, 256, 0), (20000, 64, 1, 0), (6000, 264, 700, 256)])
+def test_many_tokens_and_a_small_vocabulary(T, d, V, piece, act):
+    """dw's sum over the tokens split over workgroups."""
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V} piece={piece} {act}", flush=True)
+    rng = np.random.default_rng([T, V])
+    h, w = normal(rng, (T, d), act), normal(rng, (V, d), act, 2.0 / np.sqrt(d))
+    _check(h, w, _targets(rng, T, V, 0.2), act, piece=piece)
+
+
 def test_the_largest_tiles():
     T, d, V = 4000, 4096, 4000
     print(f"\n[gpu] vocab_loss T={T} d={d} V={V}", flush=True)
