@@ -88,6 +88,7 @@ void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v)
   v.V = D->V;
   v.bf16 = bf;
   v.piece = piece_of(D, T);
+  if (T > 2 * kVocabChunk) v.rows.chunk = c.take<int2>((T + kVocabChunk - 1) / kVocabChunk);
   v.rows.pos = c.take<int32_t>(T);
   v.rows.idx = c.take<int32_t>(T);
   v.rows.tgt = c.take<int32_t>(T);

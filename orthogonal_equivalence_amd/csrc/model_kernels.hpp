@@ -62,7 +62,9 @@ bool linear_i8(const LinearI8Desc& d, hipStream_t stream);
 // Vocabulary cross entropy (poetx_vocab_loss_*). The counted tokens (target
 // in [0, V)) are gathered to the front: compact row c is token idx[c], and
 // pos[t] is token t's compact row or -1.
+constexpr int kVocabChunk = 4096;
 struct VocabRows {
+  int2* chunk;     // [T / kVocabChunk, rounded up] counted tokens and largest gradient (more than two chunks)
   int32_t* pos;    // [T]
   int32_t* idx;    // [T]
   int32_t* tgt;    // [T] target of compact row c

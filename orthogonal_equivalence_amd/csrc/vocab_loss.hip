@@ -38,15 +38,56 @@ struct RowsArgs {
   int chunks;
 };
 
+// |v|, or 0 where it is not finite: such a gradient stays with its own token
+__device__ __forceinline__ float finite_size(float v) {
+  v = fabsf(v);
+  return v < INFINITY ? v : 0.f;
+}
+
+// Counted tokens of every kVocabChunk tokens and their largest gradient, for
+// the gather of many tokens.
+__global__ void __launch_bounds__(1024) k_vocab_count(const RowsArgs a) {
+  __shared__ int red[16];
+  __shared__ float redg[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int n = 0;
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVocabChunk / 1024; ++i) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kVocabChunk + i * 1024 + tid;
+    if (t >= a.T) break;
+    const int64_t y = a.target[t];
+    if (y < 0 || y >= a.V) continue;
+    ++n;
+    if (a.dloss) most = fmaxf(most, finite_size(a.dloss[t]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    n += __shfl_xor(n, o);
+    most = fmaxf(most, __shfl_xor(most, o));
+  }
+  if (lane == 0) {
+    red[wave] = n;
+    redg[wave] = most;
+  }
+  __syncthreads();
+  if (tid) return;
+  for (int w = 1; w < 16; ++w) {
+    n += red[w];
+    most = fmaxf(most, redg[w]);
+  }
+  a.r.chunk[blockIdx.x] = make_int2(n, __float_as_int(most));
+}
+
 // Gathers the counted tokens' rows of h to the front of hc in token order, with
 // their targets and, in the backward, their gradients and lse; a token that is
 // not counted gets zeros in its row of dh. A workgroup does `per` tokens, 64 at
-// a time, and finds its first compact row by counting the targets
-// before its own, all workgroups at the same time: no launch before this one,
-// and at most 1024 workgroups read the targets. Bound by the rows' bytes, read
-// and written once (T = 4096, d = 4096: 67 MB in 23 us, 6 of them before the
-// first row).
-template <int NW>
+// a time, and finds its first compact row by counting the targets before its
+// own, all workgroups at the same time; with CHUNKS, from the counts of
+// k_vocab_count, those of its own chunk only. Bound by the rows' bytes, read and
+// written once (T = 4096, d = 4096: 67 MB in 23 us, 6 of them before the first
+// row).
+template <int NW, bool CHUNKS>
 __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int per) {
   __shared__ int red[2][NW];
   __shared__ float redg[NW];
@@ -55,13 +96,21 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
   const int t0 = blockIdx.x * per, t1 = min(a.T, t0 + per);
   int before = 0, total = 0;
   float most = 0.f;
+  if constexpr (CHUNKS)
+    for (int k = tid; k < (a.T + kVocabChunk - 1) / kVocabChunk; k += 64 * NW) {
+      const int2 c = a.r.chunk[k];
+      total += c.x;
+      before += (k + 1) * kVocabChunk <= t0 ? c.x : 0;
+      most = fmaxf(most, __int_as_float(c.y));
+    }
 #pragma unroll 4
-  for (int t = tid; t < a.T; t += 64 * NW) {
+  for (int t = (CHUNKS ? t0 / kVocabChunk * kVocabChunk : 0) + tid; t < (CHUNKS ? t0 : a.T); t += 64 * NW) {
     const int64_t y = a.target[t];
     const int c = y >= 0 && y < a.V;
-    total += c;
     before += t < t0 ? c : 0;
-    if (a.dloss && c) most = fmaxf(most, fabsf(a.dloss[t]));
+    if constexpr (CHUNKS) continue;
+    total += c;
+    if (a.dloss && c) most = fmaxf(most, finite_size(a.dloss[t]));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -592,12 +641,17 @@ void gather_rows(const VocabDesc& D, bool backward, hipStream_t st) {
                    static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc), D.ldhc * es / 16,
                    static_cast<uint4*>(backward ? D.dh : nullptr), static_cast<int>(D.d * es / 16)};
   // a row a wave; few tokens on as many CUs as they have fours (d = 4096, NW = 4
-  // against 16: T = 1111 9.2 us, 11.3; 4096 28 us, 23; 8192 62 us, 48)
+  // against 16: T = 1111 9.2 us, 11.3; 4096 28 us, 23; 8192 62 us, 48); every
+  // workgroup reads all targets where that costs less than a launch of counts (T =
+  // 8192: 48 us against 45 + 5; T = 65536, d = 512: 107 us against 34 + 5)
   if (T <= 2048) {
-    hipLaunchKernelGGL(k_vocab_gather<4>, dim3(tiles(T, 4)), dim3(256), 0, st, a, 4);
+    hipLaunchKernelGGL((k_vocab_gather<4, false>), dim3(tiles(T, 4)), dim3(256), 0, st, a, 4);
+  } else if (T <= 2 * kVocabChunk) {
+    hipLaunchKernelGGL((k_vocab_gather<16, false>), dim3(tiles(T, 16)), dim3(1024), 0, st, a, 16);
   } else {
-    const int per = T <= 16384 ? 16 : (tiles(T, 1024) + 63) / 64 * 64;
-    hipLaunchKernelGGL(k_vocab_gather<16>, dim3(tiles(T, per)), dim3(1024), 0, st, a, per);
+    const int per = T <= 16384 ? 16 : 64;
+    hipLaunchKernelGGL(k_vocab_count, dim3(tiles(T, kVocabChunk)), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((k_vocab_gather<16, true>), dim3(tiles(T, per)), dim3(1024), 0, st, a, per);
   }
 }
 

@@ -180,6 +180,22 @@ def test_large_logits(act):
     _check(h, w, _targets(rng, 50, 700, 0.1), act)
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("T", [20, 9000])
+def test_a_gradient_that_is_not_finite_stays_with_its_token(T, bad):
+    rng = np.random.default_rng(9)
+    h, w, t = normal(rng, (T, 64), "bf16"), normal(rng, (300, 64), "bf16"), _targets(rng, T, 300, 0.0)
+    _, lse = model.vocab_loss(h, w, t)
+    dloss = normal(rng, T, "f32")
+    dloss[7] = 0
+    want, _ = model.vocab_loss_backward(h, w, t, lse, dloss)
+    dloss[7] = bad
+    got, _ = model.vocab_loss_backward(h, w, t, lse, dloss)
+    torch.cuda.synchronize()
+    keep = [i for i in range(T) if i != 7]
+    assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[7]).any()
+
+
 def test_a_row_that_is_not_finite_shows_in_its_loss_only():
     rng = np.random.default_rng(6)
     h, w, t = normal(rng, (20, 64), "bf16"), normal(rng, (300, 64), "bf16"), _targets(rng, 20, 300, 0.0)
