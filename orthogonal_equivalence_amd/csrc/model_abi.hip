@@ -80,45 +80,61 @@ int64_t piece_of(const poetx_vocab* D, int64_t T) {
   return round256((all + pieces - 1) / pieces);
 }
 
-void plan_vocab(const poetx_vocab* D, int64_t T, int op, Carve& c, VocabDesc& v) {
-  const int es = elem(D->dtype);
-  const bool bwd = op == POETX_OP_VOCAB_BACKWARD, bf = D->dtype == POETX_BF16;
+// Sizes, tiles and splits of a call, without its memory.
+VocabDesc vocab_sizes(const poetx_vocab* D, int64_t T, int op) {
+  VocabDesc v;
   v.T = T;
   v.d = D->d;
   v.V = D->V;
-  v.bf16 = bf;
+  v.bf16 = D->dtype == POETX_BF16;
   v.piece = piece_of(D, T);
+  const int es = elem(D->dtype);
+  v.ldhc = (D->d * es + 127) / 128 * 128 / es;
+  v.backward = op == POETX_OP_VOCAB_BACKWARD;
+  vocab_plan(v);
+  return v;
+}
+
+void carve_vocab(VocabDesc& v, Carve& c) {
+  const int64_t T = v.T, es = v.bf16 ? 2 : 4;
   if (T > 2 * kVocabChunk) v.rows.chunk = c.take<int2>((T + kVocabChunk - 1) / kVocabChunk);
   v.rows.pos = c.take<int32_t>(T);
   v.rows.idx = c.take<int32_t>(T);
   v.rows.tgt = c.take<int32_t>(T);
-  v.rows.g = bwd ? c.take<float>(T) : nullptr;
-  v.rows.lse = bwd ? c.take<float>(T) : nullptr;
-  v.rows.unit = bwd ? c.take<float>(1) : nullptr;
   v.rows.count = c.take<int32_t>(1);
-  v.ldhc = (D->d * es + 127) / 128 * 128 / es;
   v.hc = c.take<char>(T * v.ldhc * es);
-  if (bwd) {
+  if (v.backward) {
+    v.rows.g = c.take<float>(T);
+    v.rows.lse = c.take<float>(T);
+    v.rows.unit = c.take<float>(1);
     v.p = c.take<char>(T * v.piece * es);
-    const int64_t t = std::max<int64_t>(T, 1), rows = std::min(v.piece, D->V);
-    v.dh_plan = vocab_dh_plan(t, D->d, D->V, v.piece, bf);
-    v.dw_plan = vocab_dw_plan(t, D->d, D->V, v.piece, bf);
-    if (v.piece < D->V || v.dh_plan.splits > 1) v.acc = c.take<float>(v.dh_plan.splits * T * D->d);
-    if (v.dw_plan.splits > 1) v.acc_w = c.take<float>(v.dw_plan.splits * rows * D->d);
-    return;
+    if (v.piece < v.V || v.dh_plan.splits > 1) v.acc = c.take<float>(v.dh_plan.splits * T * v.d);
+    if (v.dw_plan.splits > 1) v.acc_w = c.take<float>(v.dw_plan.splits * std::min(v.piece, v.V) * v.d);
+  } else {
+    v.tl = c.take<float>(T);
+    v.stat = c.take<float2>(static_cast<int64_t>(v.stat_tiles) * T);
   }
-  v.tl = c.take<float>(T);
-  v.stat = c.take<float2>(vocab_stat_tiles(std::max<int64_t>(T, 1), D->V, bf) * T);
 }
 
-int vocab_common(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t ldh, const void* w, int64_t ldw,
-                 const int64_t* target, const void* ws, size_t ws_bytes) {
+// A checked call's description, its workspace laid out.
+int vocab_call(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t ldh, const void* w, int64_t ldw,
+               const int64_t* target, void* ws, size_t ws_bytes, VocabDesc& v) {
   const int es = elem(D->dtype);
   if (!stride_ok(ldh, D->d, es) || !stride_ok(ldw, D->d, es)) return POETX_EINVAL;
   if (!ptrs_ok({h, w, target})) return POETX_EINVAL;
-  if (ldw > kVocabStride || !vocab_fits(T, D->d, D->V, piece_of(D, T), D->dtype == POETX_BF16))
-    return POETX_EUNSUPPORTED;
-  return ws_ok(ws, ws_bytes, poetx_vocab_ws_bytes(D, T, op));
+  v = vocab_sizes(D, T, op);
+  if (ldw > kVocabStride || !v.fits) return POETX_EUNSUPPORTED;
+  Carve size(nullptr);
+  carve_vocab(v, size);
+  if (const int e = ws_ok(ws, ws_bytes, size.off)) return e;
+  Carve c(ws);
+  carve_vocab(v, c);
+  v.h = h;
+  v.ldh = ldh;
+  v.w = w;
+  v.ldw = ldw;
+  v.target = target;
+  return POETX_OK;
 }
 
 }  // namespace
@@ -261,9 +277,9 @@ int poetx_linear_i8_prepare(int64_t m, int64_t n, const int8_t* w0, int8_t* wt, 
 
 size_t poetx_vocab_ws_bytes(const poetx_vocab* D, int64_t T, int op) {
   if (!vocab_ok(D, T) || (op != POETX_OP_VOCAB_FORWARD && op != POETX_OP_VOCAB_BACKWARD)) return 0;
+  VocabDesc v = vocab_sizes(D, T, op);
   Carve c(nullptr);
-  VocabDesc v;
-  plan_vocab(D, T, op, c, v);
+  carve_vocab(v, c);
   return c.off;
 }
 
@@ -276,16 +292,9 @@ int poetx_vocab_loss_forward(const poetx_vocab* D, int64_t T, const void* h, int
     return POETX_OK;
   }
   if (!ptrs_ok({loss, lse})) return POETX_EINVAL;
-  if (const int e = vocab_common(D, T, POETX_OP_VOCAB_FORWARD, h, ldh, w, ldw, target, ws, ws_bytes)) return e;
-  clear_pending_error();
-  Carve c(ws);
   VocabDesc v;
-  plan_vocab(D, T, POETX_OP_VOCAB_FORWARD, c, v);
-  v.h = h;
-  v.ldh = ldh;
-  v.w = w;
-  v.ldw = ldw;
-  v.target = target;
+  if (const int e = vocab_call(D, T, POETX_OP_VOCAB_FORWARD, h, ldh, w, ldw, target, ws, ws_bytes, v)) return e;
+  clear_pending_error();
   v.loss = loss;
   v.lse = lse;
   ProfScope p("vocab_loss_fwd", stream);
@@ -303,16 +312,9 @@ int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const void* h, in
     return launch_status();
   }
   if (!ptrs_ok({lse, dh}) || (dloss && !aligned16(dloss))) return POETX_EINVAL;
-  if (const int e = vocab_common(D, T, POETX_OP_VOCAB_BACKWARD, h, ldh, w, ldw, target, ws, ws_bytes)) return e;
-  clear_pending_error();
-  Carve c(ws);
   VocabDesc v;
-  plan_vocab(D, T, POETX_OP_VOCAB_BACKWARD, c, v);
-  v.h = h;
-  v.ldh = ldh;
-  v.w = w;
-  v.ldw = ldw;
-  v.target = target;
+  if (const int e = vocab_call(D, T, POETX_OP_VOCAB_BACKWARD, h, ldh, w, ldw, target, ws, ws_bytes, v)) return e;
+  clear_pending_error();
   v.lse_in = lse;
   v.dloss = dloss;
   v.scale = scale;

@@ -77,8 +77,6 @@ struct VocabRows {
 struct KPlan {
   int tile = 0, splits = 1;
 };
-KPlan vocab_dh_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
-KPlan vocab_dw_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
 struct VocabDesc {
   const void* h = nullptr;
   int64_t ldh = 0;
@@ -86,12 +84,14 @@ struct VocabDesc {
   int64_t ldw = 0;
   const int64_t* target = nullptr;
   int64_t T = 0, d = 0, V = 0;
-  bool bf16 = true;
+  bool bf16 = true, backward = false;
+  bool fits = true;         // every product's tiles in one launch
   VocabRows rows{};
   void* hc = nullptr;       // [T][ldhc] compact rows of h
   int64_t ldhc = 0;         // whole 128-byte lines, so that a tile's rows take no more lines than they fill
   // forward
-  float2* stat = nullptr;   // [vocab_stat_tiles][T] maximum and sum of a tile's columns
+  int stat_tile = 0, stat_tiles = 0;  // tile of the product, and column tiles
+  float2* stat = nullptr;   // [stat_tiles][T] maximum and sum of a tile's columns
   float* tl = nullptr;      // [T] target's logit of a compact row
   float* loss = nullptr;
   float* lse = nullptr;
@@ -107,10 +107,8 @@ struct VocabDesc {
   void* dh = nullptr;
   void* dw = nullptr;
 };
-// Whether every product's tiles fit one launch.
-bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16);
-// Column tiles of the forward.
-int vocab_stat_tiles(int64_t T, int64_t V, bool bf16);
+// Sets the tiles, splits and `fits` from the sizes.
+void vocab_plan(VocabDesc& d);
 void vocab_forward(const VocabDesc& d, hipStream_t stream);
 void vocab_backward(const VocabDesc& d, hipStream_t stream);
 

@@ -663,23 +663,22 @@ TileArgs tile_args(const VocabDesc& D) {
   return a;
 }
 
-}  // namespace
-
-KPlan vocab_k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
-  // Tile and splits together: rounds of workgroups, each of steps / splits
-  // K steps, and the sums' bytes (d = 4096, V = 131072: dh of 16 tokens 225 us, 580
-  // unsplit; backward of 600 tokens 2.13 ms, 2.70; d = 1024, V = 32000, 64 tokens:
-  // backward 67 us, 171).
+// Tile and splits of a product together: rounds of workgroups, each of steps /
+// splits K steps, and the sums' bytes (d = 4096, V = 131072: dh of 16 tokens 225
+// us, 580 unsplit; backward of 600 tokens 2.13 ms, 2.70; d = 1024, V = 32000, 64
+// tokens: backward 67 us, 171; T = 65536, d = 512, V = 100: dw split, backward
+// 195 us, 422). Tiles that fill the CUs a few times over are not split.
+KPlan k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
   const TileCost* costs = bf16 ? kTileCosts : kTileCostsF32;
   const int kinds = bf16 ? static_cast<int>(kTileKinds) : static_cast<int>(kTileKindsF32);
-  const int64_t steps = (K + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
+  const int steps = static_cast<int>((K + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32));
   KPlan best{};
   double least = INFINITY;
   for (int t = 0; t < kinds; ++t) {
     if (bf16 && no_192 && t == kTile192x256) continue;
     const int64_t n = ((M + costs[t].bm - 1) / costs[t].bm) * ((N + costs[t].bn - 1) / costs[t].bn);
     const double step = costs[t].us / (bf16 ? 32 : 1);
-    for (int s = 1; s <= 16 && (s == 1 || steps / s >= 8); ++s) {
+    for (int s = 1; s <= 16 && (s == 1 || (steps >= 8 * s && n * s <= 4 * costs[t].slots)); ++s) {
       double us = static_cast<double>((n * s + costs[t].slots - 1) / costs[t].slots) *
                   static_cast<double>((steps + s - 1) / s) * step;
       if (s > 1) us += 4.0 + static_cast<double>(M) * static_cast<double>(N) * 8.0 * s / 4e6;
@@ -692,25 +691,24 @@ KPlan vocab_k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
   }
   return best;
 }
-KPlan vocab_dh_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
-  return vocab_k_plan(T, d, std::min(piece, V), bf16, false);
-}
-KPlan vocab_dw_plan(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
-  return vocab_k_plan(std::min(piece, V), d, T, bf16, true);
-}
 
-bool vocab_fits(int64_t T, int64_t d, int64_t V, int64_t piece, bool bf16) {
-  const TileCost* t = bf16 ? kTileCosts : kTileCostsF32;
-  const int64_t most = std::min(V, piece), last = V % piece ? V % piece : piece;
-  const KPlan h = vocab_dh_plan(T, d, V, piece, bf16), w = vocab_dw_plan(T, d, V, piece, bf16);
-  return tiles_fit(t[pick(T, V, bf16)], T, V) && tiles_fit(t[pick(T, most, bf16)], T, most) &&
-         tiles_fit(t[pick(T, last, bf16)], T, last) && tiles_fit(t[h.tile], T, d * h.splits) &&
-         tiles_fit(t[w.tile], most, d * w.splits);
-}
+}  // namespace
 
-int vocab_stat_tiles(int64_t T, int64_t V, bool bf16) {
-  const int t = pick(T, V, bf16);
-  return tiles(V, bf16 ? kTileCosts[t].bn : kTileCostsF32[t].bn);
+void vocab_plan(VocabDesc& D) {
+  const TileCost* t = D.bf16 ? kTileCosts : kTileCostsF32;
+  auto fits = [&](int tile, int64_t M, int64_t N) { D.fits = D.fits && tiles_fit(t[tile], M, N); };
+  D.fits = true;
+  D.stat_tile = pick(D.T, D.V, D.bf16);
+  D.stat_tiles = tiles(D.V, t[D.stat_tile].bn);
+  fits(D.stat_tile, D.T, D.V);  // the backward refuses what the forward does
+  if (!D.backward) return;
+  const int64_t most = std::min(D.V, D.piece), last = D.V % D.piece;
+  D.dh_plan = k_plan(D.T, D.d, most, D.bf16, false);
+  D.dw_plan = k_plan(most, D.d, D.T, D.bf16, true);
+  fits(pick(D.T, most, D.bf16), D.T, most);
+  if (last) fits(pick(D.T, last, D.bf16), D.T, last);
+  fits(D.dh_plan.tile, D.T, D.d * D.dh_plan.splits);
+  fits(D.dw_plan.tile, most, D.d * D.dw_plan.splits);
 }
 
 void vocab_forward(const VocabDesc& D, hipStream_t st) {
@@ -722,8 +720,8 @@ void vocab_forward(const VocabDesc& D, hipStream_t st) {
   a.vn = static_cast<int>(D.V);
   a.stat = D.stat;
   a.tl = D.tl;
-  const int t = pick(D.T, D.V, D.bf16);
-  a.tiles_n = vocab_stat_tiles(D.T, D.V, D.bf16);
+  const int t = D.stat_tile;
+  a.tiles_n = D.stat_tiles;
   with_logits_tile(D.bf16, kernel_of(t, D.bf16), D.d, [&](auto cfg) {
     using C = decltype(cfg);
     hipLaunchKernelGGL((k_vocab_stat<C>), dim3(pick_count(t, D.T, D.V, D.bf16)), dim3(C::NT), 0, st, a);
