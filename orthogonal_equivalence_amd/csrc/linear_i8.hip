@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
   const int n0 = blockIdx.x * 32 * OB;
   char* ring = smem + wave * D * C::PIECE;
 
-  TileLoader<32 * OB, 4 * OB, true, 1, true> lw;
-  TileLoader<32 * TT, 4 * TT, true, 1, true> lx;
+  TileLoader<32 * OB, 4 * OB, true, 1, true, 32> lw;
+  TileLoader<32 * TT, 4 * TT, true, 1, true, 32> lx;
   lw.init(a.w, n0, 0, 0, lane);
   lx.init(a.x, 0, 0, 0, lane);
   const int pieces = (a.m + 127) / 128;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[t][o][i] = 0;
   const int r = lane & 31, half = lane >> 5;
-  const int sw = (r & 7) ^ ((r >> 3) & 1);
+  const int sw = chunk_swizzle<32>(r);
 
 #pragma unroll
   for (int s = 0; s < D - 1; ++s) load(wave + s * NW, ring + s * C::PIECE);

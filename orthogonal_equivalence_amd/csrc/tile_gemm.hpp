@@ -9,8 +9,10 @@
 //    past the end of K get an offset outside the buffer for the same effect
 //    (what lies between rows may be anything, NaN too).
 //  * LDS rows of a K-contiguous operand are 128 bytes, chunk c of row r in
-//    slot c ^ (r & 7) ^ ((r >> 3) & 1): the 16 rows of a fragment read fall on
-//    all banks evenly.
+//    slot c ^ (r & 7): a fragment's 16-byte reads then never meet in a bank
+//    (conflicts 0.1% of the LDS cycles; with the order for 32-row fragments,
+//    which also turns with r / 8, 50%, though large products, bound by power,
+//    took the same time).
 //  * An operand stored with K as its rows (A[k][m], B[k][n]) lies in LDS as it
 //    does in memory. bfloat16 is read with ds_read_b64_tr_b16, which hands
 //    every lane four consecutive k of its own column, float word by word;
@@ -167,9 +169,16 @@ __device__ __forceinline__ int row_swizzle(int r) {
   else return ((r & 3) << 2) ^ (((r >> 3) & 1) << 1);
 }
 
+// Slot of chunk c in row r of a K-contiguous tile: c ^ chunk_swizzle(r), for
+// fragments of FR rows.
+template <int FR>
+__device__ __forceinline__ int chunk_swizzle(int r) {
+  return FR == 16 ? r & 7 : (r & 7) ^ ((r >> 3) & 1);
+}
+
 // The loads of one operand tile: per-lane byte offsets from the tile's first
 // byte, and the tile's buffer.
-template <int BT, int L, bool KC, int ES, bool KTAIL>
+template <int BT, int L, bool KC, int ES, bool KTAIL, int FR = 16>
 struct TileLoader {
   const char* base;     // first byte of the tile's stored rows at k = 0
   int64_t left;         // bytes from there to the operand's end
@@ -189,7 +198,7 @@ struct TileLoader {
 #pragma unroll
       for (int i = 0; i < L; ++i) {
         const int r = (wave * L + i) * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ (r & 7) ^ ((r >> 3) & 1);
+        const int c = (lane & 7) ^ chunk_swizzle<FR>(r);
         voff[i] = static_cast<uint32_t>(r * ldb) + c * 16;
         if constexpr (KTAIL) vtail[i] = c * 16 < kend ? voff[i] : 0xfffffff0u;
       }
@@ -343,7 +352,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
   // fragment addresses: K group kk of a K-contiguous row is chunk 4 kk +
   // lane / 16 (64 bytes of K)
   const int lrow = lane & 15;
-  const int sw = (lrow & 7) ^ ((lrow >> 3) & 1);
+  const int sw = chunk_swizzle<16>(lrow);
   int koff[2];
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) koff[kk] = lrow * 128 + (((4 * kk + (lane >> 4)) ^ sw) << 4);

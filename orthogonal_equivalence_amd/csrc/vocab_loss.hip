@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_vocab_stat(const TileArgs a) {
 
 // lse and loss of every token from the tiles' pairs: N tokens a workgroup, 1024
 // / N threads a token over the tiles. Bound by latencies: 8 tokens (a row's
-// pairs of one 64-byte piece) where there are tiles for their threads, else 64
-// (T = 16, 2048 tiles: 8 us, 64 tokens 25; T = 40000, one tile: 22 us and 5).
+// pairs of one 64-byte piece) for few tokens with tiles for that many threads,
+// else 64 (T = 16, 2048 tiles: 8 us, 64 tokens 25; T = 8192, 512 tiles: 16 us
+// and 10; T = 40000, one tile: 22 us and 5).
 template <int N>
 __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int tiles, const float* tl, const int32_t* pos,
                                                      int T, float* loss, float* lse) {
@@ -730,7 +731,7 @@ void vocab_forward(const VocabDesc& D, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(tiles(D.T, tokens)), dim3(1024), 0, st, D.stat, a.tiles_n, D.tl, D.rows.pos, T,
                        D.loss, D.lse);
   };
-  if (a.tiles_n >= 128) join(k_vocab_join<8>, 8);
+  if (T <= 2048 && a.tiles_n >= 128) join(k_vocab_join<8>, 8);
   else join(k_vocab_join<64>, 64);
 }
 
