@@ -145,7 +145,8 @@ POETX_API int poetx_vocab_loss_forward(const poetx_vocab* D, int64_t T, const vo
  *   lse [T] as the forward wrote it; dh [T][d], dw [V][d] overwritten.
  * With dtype POETX_BF16, dl is rounded to bfloat16 before the two products (at
  * most 2^-8 relative each, independent from term to term of their sums), in
- * units of the largest |g[t]|, which is applied to the sums in float32. */
+ * units of the largest finite |g[t]|, which is applied to the sums in float32; a
+ * g[t] that is not finite reaches its own row of dh, and dw. */
 POETX_API int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const void* h, int64_t ldh, const void* w,
                                         int64_t ldw, const int64_t* target, const float* lse, const float* dloss,
                                         float scale, void* dh, void* dw, void* ws, size_t ws_bytes,

@@ -320,8 +320,8 @@ __device__ __forceinline__ void row_read(const char* tile, const uint32_t* a, in
 }
 
 // The wave's TM x TN tiles of 16 x 16 of the workgroup's tile at (m0, n0),
-// over K steps [it0, it1). smem: Cfg::LDS bytes, free
-// again for the caller when this returns (after its barrier).
+// over K steps [it0, it1). lds: Cfg::LDS bytes, free again for the caller when
+// this returns (after its barrier).
 template <class Cfg>
 __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOperand& B, int m0, int n0,
                                              int it0, int it1, char* lds,
@@ -407,10 +407,10 @@ __device__ __forceinline__ void tile_product(const TileOperand& A, const TileOpe
     }
   };
 
-  // The loads of a stage: N3 in the last phase of the step that frees its
-  // slot, the others in the next step's first. Steps past the last
-  // load the last slice again, into slots that are idle by then, so that the
-  // same number of loads is always in flight.
+  // The loads of a stage: N3 in the last phase of the step that frees its slot,
+  // the others in the next step's first. Steps past the last load the last slice
+  // again, into slots that are idle by then, so that the same number of loads is
+  // always in flight.
   constexpr int L = LA + LB, N3 = (L + 1) / 2;
   auto step_of = [&](int it) { return min(it + group, it1 - 1); };
   auto load = [&](int i, int pf, char* to) {
