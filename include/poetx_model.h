@@ -15,7 +15,8 @@
  *    elements needs ld >= cols, and every row has to start on a 16-byte
  *    boundary (ld a multiple of 8 for bfloat16, of 4 for float, of 16 for
  *    int8). Matrices without a stride argument are contiguous. Every pointer
- *    is 16-byte aligned.
+ *    is 16-byte aligned, but those to one value a token (target, loss, lse,
+ *    dloss, rstd, q_scale, x_scale), which are aligned as their type.
  *  - Outputs must not overlap inputs or each other unless stated otherwise.
  *  - T = 0 tokens succeed (and write what does not depend on tokens: zero
  *    gradients of parameters).

@@ -20,6 +20,13 @@ int elem(int dtype) { return dtype == POETX_F32 ? 4 : (dtype == POETX_BF16 ? 2 :
 
 bool rows_ok(int64_t T, int64_t n, int mult) { return T >= 0 && T <= kMaxRows && n >= mult && n <= kMaxWidth && n % mult == 0; }
 
+// values one a token, read one at a time: aligned as their type
+bool tokens_ok(std::initializer_list<const void*> ps, uintptr_t size) {
+  for (const void* p : ps)
+    if (!p || reinterpret_cast<uintptr_t>(p) % size) return false;
+  return true;
+}
+
 // a row stride: at least the row, every row 16-byte aligned
 bool stride_ok(int64_t ld, int64_t cols, int es) { return ld >= cols && ld <= (int64_t(1) << 40) && ld * es % 16 == 0; }
 
@@ -121,7 +128,7 @@ int vocab_call(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t l
                const int64_t* target, void* ws, size_t ws_bytes, VocabDesc& v) {
   const int es = elem(D->dtype);
   if (!stride_ok(ldh, D->d, es) || !stride_ok(ldw, D->d, es)) return POETX_EINVAL;
-  if (!ptrs_ok({h, w, target})) return POETX_EINVAL;
+  if (!ptrs_ok({h, w}) || !tokens_ok({target}, 8)) return POETX_EINVAL;
   v = vocab_sizes(D, T, op);
   if (ldw > kVocabStride || !v.fits) return POETX_EUNSUPPORTED;
   Carve size(nullptr);
@@ -146,7 +153,7 @@ int poetx_rmsnorm_forward(int64_t T, int64_t n, int dtype, const void* x, int64_
   if (!rows_ok(T, n, 8)) return POETX_EINVAL;
   NormFwdDesc d;
   if (const int e = norm_common(T, n, dtype, x, ldx, res, ldr, gain, eps, h, d)) return e;
-  if (T > 0 && (!ptrs_ok({y}) || (rstd && !aligned16(rstd)))) return POETX_EINVAL;
+  if (T > 0 && (!ptrs_ok({y}) || (rstd && !tokens_ok({rstd}, 4)))) return POETX_EINVAL;
   clear_pending_error();
   if (T == 0) return POETX_OK;
   d.y = y;
@@ -162,7 +169,7 @@ int poetx_rmsnorm_forward_q8(int64_t T, int64_t n, int dtype, const void* x, int
   if (!rows_ok(T, n, 16)) return POETX_EINVAL;
   NormFwdDesc d;
   if (const int e = norm_common(T, n, dtype, x, ldx, res, ldr, gain, eps, h, d)) return e;
-  if (T > 0 && !ptrs_ok({q, q_scale})) return POETX_EINVAL;
+  if (T > 0 && (!ptrs_ok({q}) || !tokens_ok({q_scale}, 4))) return POETX_EINVAL;
   clear_pending_error();
   if (T == 0) return POETX_OK;
   d.q = q;
@@ -175,7 +182,7 @@ int poetx_rmsnorm_forward_q8(int64_t T, int64_t n, int dtype, const void* x, int
 int poetx_quantize_rows(int64_t T, int64_t n, int dtype, const void* x, int64_t ldx, int8_t* q, float* q_scale,
                         hipStream_t stream) {
   if (!rows_ok(T, n, 16) || !act_ok(dtype) || !stride_ok(ldx, n, elem(dtype))) return POETX_EINVAL;
-  if (T > 0 && !ptrs_ok({x, q, q_scale})) return POETX_EINVAL;
+  if (T > 0 && (!ptrs_ok({x, q}) || !tokens_ok({q_scale}, 4))) return POETX_EINVAL;
   clear_pending_error();
   if (T == 0) return POETX_OK;
   NormFwdDesc d;
@@ -203,7 +210,7 @@ int poetx_rmsnorm_backward(int64_t T, int64_t n, int dtype, const void* dy, int6
   if (!stride_ok(lddy, n, elem(dtype)) || (dh && !stride_ok(lddh, n, elem(dtype)))) return POETX_EINVAL;
   if (dgain && !aligned16(dgain)) return POETX_EINVAL;
   if (T > 0) {
-    if (!ptrs_ok({dy, h, rstd, gain, dx}) || (dh && !aligned16(dh))) return POETX_EINVAL;
+    if (!ptrs_ok({dy, h, gain, dx}) || !tokens_ok({rstd}, 4) || (dh && !aligned16(dh))) return POETX_EINVAL;
     if (!alias_ok(dx, dy, lddy, n) || (dh && !alias_ok(dx, dh, lddh, n))) return POETX_EINVAL;
     if (dgain)
       if (const int e = ws_ok(ws, ws_bytes, poetx_rmsnorm_ws_bytes(T, n))) return e;
@@ -246,7 +253,7 @@ int poetx_linear_i8(int64_t T, int64_t m, int64_t n, int out_dtype, const int8_t
                     const int8_t* wt, const float* w_scale, void* z, int64_t ldz, hipStream_t stream) {
   if (!i8_sizes_ok(m, n) || T < 0 || T > kVocabTokens || !act_ok(out_dtype)) return POETX_EINVAL;
   if (!stride_ok(ldz, n, elem(out_dtype))) return POETX_EINVAL;
-  if (T > 0 && !ptrs_ok({xq, x_scale, wt, w_scale, z})) return POETX_EINVAL;
+  if (T > 0 && (!ptrs_ok({xq, wt, w_scale, z}) || !tokens_ok({x_scale}, 4))) return POETX_EINVAL;
   clear_pending_error();
   if (T == 0) return POETX_OK;
   LinearI8Desc d;
@@ -291,7 +298,7 @@ int poetx_vocab_loss_forward(const poetx_vocab* D, int64_t T, const void* h, int
     clear_pending_error();
     return POETX_OK;
   }
-  if (!ptrs_ok({loss, lse})) return POETX_EINVAL;
+  if (!tokens_ok({loss, lse}, 4)) return POETX_EINVAL;
   VocabDesc v;
   if (const int e = vocab_call(D, T, POETX_OP_VOCAB_FORWARD, h, ldh, w, ldw, target, ws, ws_bytes, v)) return e;
   clear_pending_error();
@@ -311,7 +318,7 @@ int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const void* h, in
     fill_zero_f32(static_cast<float*>(dw), D->V * D->d * elem(D->dtype) / 4, stream);
     return launch_status();
   }
-  if (!ptrs_ok({lse, dh}) || (dloss && !aligned16(dloss))) return POETX_EINVAL;
+  if (!ptrs_ok({dh}) || !tokens_ok({lse}, 4) || (dloss && !tokens_ok({dloss}, 4))) return POETX_EINVAL;
   VocabDesc v;
   if (const int e = vocab_call(D, T, POETX_OP_VOCAB_BACKWARD, h, ldh, w, ldw, target, ws, ws_bytes, v)) return e;
   clear_pending_error();

@@ -89,6 +89,15 @@ def test_scales_that_are_not_finite_stay_in_their_row_or_column():
     assert torch.isfinite(z[rows][:, cols]).all()
 
 
+@pytest.mark.parametrize("T", [1, 5, 100])
+def test_some_of_the_tokens_and_outputs(T):
+    xq, xs, wt, ws = _case(T + 7, 272, 528)
+    z = model.linear_i8(xq, xs, wt, ws)
+    part = model.linear_i8(xq[7:], xs[7:], wt[16:], ws[16:])
+    torch.cuda.synchronize()
+    assert torch.equal(part, z[7:, 16:])
+
+
 def test_no_tokens():
     xq, xs, wt, ws = _case(1, 64, 64)
     assert model.linear_i8(xq[:0], xs[:0], wt, ws).shape == (0, 64)

@@ -96,6 +96,16 @@ def test_no_residual_and_the_stream_itself():
     within("dx", dx, DX, U16 * np.abs(DX) + 1e-5)
 
 
+def test_rstd_of_some_of_the_tokens():
+    rng = np.random.default_rng(12)
+    x, gain, dy = normal(rng, (9, 640), "bf16"), normal(rng, 640, "f32"), normal(rng, (9, 640), "bf16")
+    _, _, rstd = model.rms_norm(x, gain)
+    got = model.rms_norm_backward(dy[3:], x[3:], rstd[3:], gain)
+    want = model.rms_norm_backward(dy[3:].clone(), x[3:].clone(), rstd[3:].clone(), gain)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_strided_stream_without_a_residual():
     rng = np.random.default_rng(8)
     x, gain, dy = strided(normal(rng, (9, 640), "bf16"), 8), normal(rng, 640, "f32"), normal(rng, (9, 640), "bf16")

@@ -196,6 +196,22 @@ def test_a_gradient_that_is_not_finite_stays_with_its_token(T, bad):
     assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[7]).any()
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_slices_of_targets_and_gradients(act):
+    """Targets as a token sequence shifted by one, loss gradients from the middle of a tensor."""
+    rng = np.random.default_rng(10)
+    h, w = normal(rng, (33, 72), act), normal(rng, (300, 72), act)
+    ids, g = _targets(rng, 34, 300, 0.2), normal(rng, 36, "f32")
+    t, dloss = ids[1:], g[3:]
+    want = _check(h, w, t.clone(), act, dloss.clone())
+    lse = torch.empty(34, device="cuda")[1:]
+    lse.copy_(want[1])
+    loss2, _ = model.vocab_loss(h, w, t)
+    got = model.vocab_loss_backward(h, w, t, lse, dloss)
+    torch.cuda.synchronize()
+    assert torch.equal(loss2, want[0]) and all(torch.equal(a, b) for a, b in zip(got, want[2:]))
+
+
 def test_a_row_that_is_not_finite_shows_in_its_loss_only():
     rng = np.random.default_rng(6)
     h, w, t = normal(rng, (20, 64), "bf16"), normal(rng, (300, 64), "bf16"), _targets(rng, 20, 300, 0.0)
