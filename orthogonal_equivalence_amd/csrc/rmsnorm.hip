@@ -81,6 +81,7 @@ __device__ __forceinline__ void store_codes8(int8_t* p, const float (&v)[8], flo
 // the calls), so that one barrier a call is enough.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
+  static_assert(TPR <= 64 || TPR >= 256, "a row over several waves has the workgroup to itself");
 #pragma unroll
   for (int o = TPR < 64 ? TPR / 2 : 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   if constexpr (TPR > 64) {
