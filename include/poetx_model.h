@@ -113,6 +113,9 @@ POETX_API int poetx_linear_i8_prepare(int64_t m, int64_t n, const int8_t* w0, in
  * w [V][d]. The logits are formed tile by tile and not kept: the forward
  * keeps a maximum and a sum per row, the backward forms them again, piece by
  * piece of the vocabulary, and multiplies each piece's gradient out at once.
+ * The loss is formed as (max_v l[t][v] - l[t][target[t]]) + log sum_v exp(l[t][v]
+ * - max): two terms of at least 0, so that it is never negative and the rounding
+ * of a large lse is not in it.
  * A token whose target is outside [0, V) (such as -100) is not counted: its
  * loss, lse and dh are 0, it adds nothing to dw, and its row of h is never
  * used, whatever it holds.

@@ -290,12 +290,12 @@ __device__ __forceinline__ float exp_rel(float l, float ref2) {
   return __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -ref2));
 }
 
-// Joins (m, s) with (m2, s2): sums of 2^(x - m) over disjoint sets. An empty
-// set is (-inf, 0).
+// Joins (m, s) with (m2, s2): sums of exp(x - m) over disjoint sets whose largest
+// is m. An empty set is (-inf, 0), any other s at least 1.
 __device__ __forceinline__ void join_stat(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   const float ref = top == -INFINITY ? 0.f : top;
-  s = s * __builtin_amdgcn_exp2f(m - ref) + s2 * __builtin_amdgcn_exp2f(m2 - ref);
+  s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - ref) * kLog2e);
   // a NaN logit leaves its mark in the sum; fmaxf drops it
   m = top;
 }
@@ -315,10 +315,12 @@ __device__ __forceinline__ void mask_columns(f32x4_t (&acc)[Cfg::TM][Cfg::TN], i
     }
 }
 
-// Maximum and sum of every row over the tile's columns, in powers of two, and
-// the targets' logits. The exponentials come from the sums as they lie in the
-// registers (T = 8192, d = 4096, V = 131072: 6.4 ms, 1.38 PFLOP/s, matrix cores
-// busy in 72% of the cycles).
+// Maximum and sum of every row over the tile's columns, and the targets' logits.
+// The exponentials come from the sums as they lie in the registers (T = 8192, d
+// = 4096, V = 131072: 6.4 ms, 1.38 PFLOP/s, matrix cores busy in 72% of the
+// cycles), one fused step each against the maximum in powers of two. What that
+// reference's rounding puts on all of them alike (1e-5 of them at logits of 200)
+// is taken out of their sum.
 template <class Cfg>
 __device__ __forceinline__ void stat_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
@@ -353,14 +355,16 @@ __device__ __forceinline__ void stat_tile(const TileArgs& a, int bid, int count,
         for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      m *= kLog2e;
-      const float ref = m == -INFINITY ? 0.f : m;
+      const bool none = m == -INFINITY;
+      const float ref = none ? 0.f : m * kLog2e, ref_off = none ? 0.f : fmaf(m, kLog2e, -ref);
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) s += exp_rel(acc[i][j][r], ref);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
+      s *= __builtin_amdgcn_exp2f(-ref_off);
+      if (!none && s < 1.f) s = 1.f;  // the maximum's own term (a NaN stays)
       if (lane < 16) red[wn * Cfg::BM + row] = make_float2(m, s);
     }
   }
@@ -389,7 +393,10 @@ __global__ void __launch_bounds__(C::NT, 1) k_vocab_stat(const TileArgs a) {
   }
 }
 
-// lse and loss of every token from the tiles' pairs: N tokens a workgroup, 1024
+// lse = m + log s and loss = (m - l[target]) + log s of every token from the
+// tiles' pairs: two terms that are never negative, and exact where the target is
+// the maximum (lse less the target's logit would cancel to the rounding of lse,
+// 1.5e-5 and of either sign at logits of 200). N tokens a workgroup, 1024
 // / N threads a token over the tiles. Bound by latencies: 8 tokens (a row's
 // pairs of one 64-byte piece) for few tokens with tiles for that many threads,
 // else 64 (T = 16, 2048 tiles: 8 us, 64 tokens 25; T = 8192, 512 tiles: 16 us
@@ -415,9 +422,9 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
   if (threadIdx.x >= N || t >= T) return;
 #pragma unroll
   for (int w = 1; w < 16; ++w) join_stat(m, s, red[w][lane].x, red[w][lane].y);
-  const float l = c >= 0 ? (m + __builtin_amdgcn_logf(s)) * kLn2 : 0.f;
-  lse[t] = l;
-  loss[t] = c >= 0 ? l - tl[c] : 0.f;
+  const float log_s = __builtin_amdgcn_logf(s) * kLn2;
+  lse[t] = c >= 0 ? m + log_s : 0.f;
+  loss[t] = c >= 0 ? (m - tl[c]) + log_s : 0.f;
 }
 
 // Gradient of the logits of a piece in the storage type, without the common
