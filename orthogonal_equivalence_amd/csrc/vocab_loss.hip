@@ -431,8 +431,12 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
 // factor `unit`, which the products' epilogues put back in float32: a factor
 // rounded with the target's entries, which outweigh the rest, would shift all
 // of them alike (with g = 1 / count in bfloat16, 0.3% of dh and dw in place of
-// 0.17%). p [count][ldp], zero
-// in the columns past the vocabulary.
+// 0.17%). p [count][ldp], zero in the columns past the vocabulary.
+//
+// The probabilities are exponentials against lse in powers of two, whose rounding
+// (1e-5 of them at an lse of 200) is taken out through g, one factor a row. The
+// target's p - 1 is then off by the float lse's own half step; where that takes
+// it past 0, it is 0, as p is at most 1.
 template <class Cfg>
 __device__ __forceinline__ void dlogits_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
@@ -451,16 +455,21 @@ __device__ __forceinline__ void dlogits_tile(const TileArgs& a, int bid, int cou
     const bool in = row < count;
     const int at = in ? row : m0;  // rows past the count are not stored
     const int tcol = a.r.tgt[at] - a.v0 - n0;
-    const float ref = a.r.lse[at] * kLog2e, g = a.r.g[at];
+    const float lse = a.r.lse[at], ref = lse * kLog2e, ref_off = fmaf(lse, kLog2e, -ref);
+    const float g = a.r.g[at], gp = fabsf(ref) < INFINITY ? g * __builtin_amdgcn_exp2f(-ref_off) : g;
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = g * exp_rel(acc[i][j][r], ref);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = gp * exp_rel(acc[i][j][r], ref);
     if (__any(static_cast<unsigned>(tcol - wn * Cfg::WTN) < Cfg::WTN)) {
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] -= tile_col<Cfg>(wn, lane, j, r) == tcol ? g : 0.f;
+        for (int r = 0; r < 4; ++r) {
+          if (tile_col<Cfg>(wn, lane, j, r) != tcol) continue;
+          const float dl = acc[i][j][r] - g;
+          acc[i][j][r] = (g > 0.f && dl > 0.f) || (g < 0.f && dl < 0.f) ? 0.f : dl;  // NaN stays
+        }
     }
   }
   mask_columns<Cfg>(acc, wn, lane, a.vn - n0, 0.f);

@@ -82,6 +82,22 @@ def test_small_and_large_losses_beside_large_logits(at, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_the_targets_term_of_a_sure_token_keeps_its_sign(sign, act):
+    """dl = g (p - 1) at the target, read off dw through the features that mark
+    the tokens: between 0 and the rounding of lse, never past 0."""
+    T, V = 100, 700
+    h, w, t = _case(T, V, 112, act, (60.0, 300.0), (-1.0, 0.0), 1)
+    _, lse = model.vocab_loss(h, w, t)
+    dloss = torch.full((T,), sign, device="cuda")
+    _, dw = model.vocab_loss_backward(h, w, t, lse, dloss)
+    torch.cuda.synchronize()
+    dl = sign * f64(dw)[int(t[0]), 8:8 + T]
+    assert dl.max() <= 0.0
+    assert np.all(dl >= -1.01 * U32 * (np.abs(f64(lse)) + 16))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_infinities_in_the_vocabulary_stay_as_the_formula_has_them(act):
     """A word at minus infinity takes no part; a token without a finite logit,
     or with one at infinity, has no finite loss."""
