@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(1024) k_vocab_count(const RowsArgs a) {
     const int64_t y = a.target[t];
     if (y < 0 || y >= a.V) continue;
     ++n;
-    if (a.dloss) most = fmaxf(most, finite_size(a.dloss[t]));
+    if (a.dloss) most = fmaxf(most, finite_size(a.scale * a.dloss[t]));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
     before += t < t0 ? c : 0;
     if constexpr (CHUNKS) continue;
     total += c;
-    if (a.dloss && c) most = fmaxf(most, finite_size(a.dloss[t]));
+    if (a.dloss && c) most = fmaxf(most, finite_size(a.scale * a.dloss[t]));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
   }
   if (blockIdx.x == 0 && tid == 0) {
     *a.r.count = total;
-    if (a.lse_in) *a.r.unit = a.dloss ? a.scale * most : a.scale / static_cast<float>(max(total, 1));
+    if (a.lse_in) *a.r.unit = a.dloss ? most : a.scale / static_cast<float>(max(total, 1));
   }
   for (int b = t0; b < t1; b += 64) {
     // every wave numbers the 64 tokens alike; the first writes
@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
         a.r.idx[p] = t;
         a.r.tgt[p] = static_cast<int>(y);
         if (a.lse_in) {
-          a.r.g[p] = a.dloss ? (most == 0.f ? a.dloss[t] : a.dloss[t] / most) : 1.f;
+          const float g = a.dloss ? a.scale * a.dloss[t] : 1.f;
+          a.r.g[p] = a.dloss && most != 0.f ? g / most : g;
           a.r.lse[p] = a.lse_in[t];
         }
       }
