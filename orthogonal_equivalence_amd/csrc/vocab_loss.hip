@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
   }
   if (blockIdx.x == 0 && tid == 0) {
     *a.r.count = total;
-    if (a.lse_in) *a.r.unit = a.dloss ? most : a.scale / static_cast<float>(max(total, 1));
+    // with no token counted the sums are empty, and 0 whatever the scale
+    if (a.lse_in) *a.r.unit = a.dloss ? most : total ? a.scale / static_cast<float>(total) : 0.f;
   }
   for (int b = t0; b < t1; b += 64) {
     // every wave numbers the 64 tokens alike; the first writes

@@ -34,3 +34,16 @@ def test_a_gradient_that_the_scale_takes_past_the_range_stays_with_its_token(T, 
     keep = [i for i in range(T) if i != 7]
     assert torch.isfinite(want).all()
     assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[7]).any()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_no_token_counted_adds_nothing_whatever_the_scale(scale, act):
+    rng = np.random.default_rng(4)
+    h, w = normal(rng, (40, 64), act), normal(rng, (300, 64), act)
+    t = torch.full((40,), -100, dtype=torch.int64, device="cuda")
+    _, lse = model.vocab_loss(h, w, t)
+    for dloss in (None, torch.ones(40, device="cuda")):
+        dh, dw = model.vocab_loss_backward(h, w, t, lse, dloss, scale)
+        torch.cuda.synchronize()
+        assert torch.all(dh == 0) and torch.all(dw == 0)
