@@ -73,6 +73,19 @@ struct FewCfg {
   static_assert(LDS <= 160 * 1024 && (D - 1) * L <= 63, "ring");
 };
 
+// Waits until no more than the last k pieces' loads (of L each, k up to K, the
+// same for a whole wave) are in flight.
+template <int L, int K>
+__device__ __forceinline__ void wait_pieces(int k) {
+  if constexpr (K > 0) {
+    if (k < K) {
+      wait_pieces<L, K - 1>(k);
+      return;
+    }
+  }
+  tg_wait_vm<K * L>();
+}
+
 template <int OB, int TT, int NW, int D, typename O>
 __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
   using C = FewCfg<OB, TT, NW, D>;
@@ -87,8 +100,9 @@ __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
   lw.init(a.w, n0, 0, 0, lane);
   lx.init(a.x, 0, 0, 0, lane);
   const int pieces = (a.m + 127) / 128;
-  // past the last piece nothing is in range: zeros, no memory read
+  // none past the last piece, where a row's bytes would run on into the next row
   auto load = [&](int p, char* to) {
+    if (p >= pieces) return;
 #pragma unroll
     for (int i = 0; i < 4 * OB; ++i) lw.load(i, p, to, 0);
 #pragma unroll
@@ -112,7 +126,7 @@ __global__ void __launch_bounds__(64 * NW) k_linear_i8_few(const I8Args a) {
     // the slot read in the last turn is free once its reads are done
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     load(p + (D - 1) * NW, ring + (cur == 0 ? D - 1 : cur - 1) * C::PIECE);
-    tg_wait_vm<(D - 1) * C::L>();
+    wait_pieces<C::L, D - 1>((pieces - 1 - p) / NW);
     const char* st = ring + cur * C::PIECE;
     cur = cur == D - 1 ? 0 : cur + 1;
 #pragma unroll
