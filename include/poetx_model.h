@@ -133,7 +133,11 @@ typedef struct poetx_vocab {
 enum { POETX_OP_VOCAB_FORWARD = 0, POETX_OP_VOCAB_BACKWARD = 1 };
 
 /* Workspace bytes of the two entry points below; 0 for an invalid descriptor,
- * token count or op. */
+ * token count or op. Fewer tokens can take more (their sums are split over more
+ * workgroups), yet a workspace of the size for T tokens serves every smaller
+ * count: with less than the size for their own, the entry points take a plan that
+ * fits, slower and with sums in another order, and refuse only what none fits
+ * (POETX_EWORKSPACE). */
 POETX_API size_t poetx_vocab_ws_bytes(const poetx_vocab* D, int64_t T, int op);
 
 /*   h [T][d] (stride ldh), w [V][d] (stride ldw), target [T] int64.

@@ -77,28 +77,34 @@ bool vocab_ok(const poetx_vocab* D, int64_t T) {
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
+// pieces of at most `most` rows, a multiple of 256, evened out
+int64_t even_piece(int64_t all, int64_t most) {
+  const int64_t pieces = (all + most - 1) / most;
+  return round256((all + pieces - 1) / pieces);
+}
+
 // Vocabulary rows of a piece: as asked, or as many as kPieceBytes hold (at
 // least 1024), evened out over the pieces.
 int64_t piece_of(const poetx_vocab* D, int64_t T) {
   const int64_t all = round256(D->V);
   if (D->piece > 0) return std::min({round256(D->piece), all, kPieceMax});
   const int64_t most = std::min(kPieceMax, std::max<int64_t>(1024, kPieceBytes / (std::max<int64_t>(T, 1) * elem(D->dtype)) / 256 * 256));
-  const int64_t pieces = (all + most - 1) / most;
-  return round256((all + pieces - 1) / pieces);
+  return even_piece(all, most);
 }
 
-// Sizes, tiles and splits of a call, without its memory.
-VocabDesc vocab_sizes(const poetx_vocab* D, int64_t T, int op) {
+// Sizes, tiles and splits of a call, without its memory. `lean`: the plan that
+// takes the least memory with pieces of this size.
+VocabDesc vocab_sizes(const poetx_vocab* D, int64_t T, int op, int64_t piece, bool lean) {
   VocabDesc v;
   v.T = T;
   v.d = D->d;
   v.V = D->V;
   v.bf16 = D->dtype == POETX_BF16;
-  v.piece = piece_of(D, T);
+  v.piece = piece;
   const int es = elem(D->dtype);
   v.ldhc = (D->d * es + 127) / 128 * 128 / es;
   v.backward = op == POETX_OP_VOCAB_BACKWARD;
-  vocab_plan(v);
+  vocab_plan(v, lean);
   return v;
 }
 
@@ -123,17 +129,39 @@ void carve_vocab(VocabDesc& v, Carve& c) {
   }
 }
 
+size_t vocab_bytes(VocabDesc v) {
+  Carve c(nullptr);
+  carve_vocab(v, c);
+  return c.off;
+}
+
+// The plan for a workspace of `bytes`: the fastest one, whose size the query
+// returns, or where that is larger the lean one, in smaller pieces if need be. A
+// workspace of the fastest plan for more tokens always holds it: that plan's
+// piece with these tokens takes no more in any part, as all parts grow with T.
+VocabDesc vocab_within(const poetx_vocab* D, int64_t T, int op, size_t bytes) {
+  VocabDesc v = vocab_sizes(D, T, op, piece_of(D, T), false);
+  if (!v.fits || vocab_bytes(v) <= bytes) return v;
+  v = vocab_sizes(D, T, op, v.piece, true);
+  const size_t need = vocab_bytes(v);
+  if (need <= bytes || !v.backward || D->piece > 0) return v;
+  // what the plan holds beside the piece, dh's sums over pieces included
+  const size_t row = static_cast<size_t>(T) * elem(D->dtype);
+  const size_t sums = v.piece < v.V ? 0 : static_cast<size_t>(round256(T * v.d * 4));
+  const size_t rest = need - static_cast<size_t>(v.piece) * row + sums;
+  const int64_t most = bytes > rest ? static_cast<int64_t>((bytes - rest) / row / 256 * 256) : 0;
+  return most > 0 ? vocab_sizes(D, T, op, even_piece(round256(v.V), most), true) : v;
+}
+
 // A checked call's description, its workspace laid out.
 int vocab_call(const poetx_vocab* D, int64_t T, int op, const void* h, int64_t ldh, const void* w, int64_t ldw,
                const int64_t* target, void* ws, size_t ws_bytes, VocabDesc& v) {
   const int es = elem(D->dtype);
   if (!stride_ok(ldh, D->d, es) || !stride_ok(ldw, D->d, es)) return POETX_EINVAL;
   if (!ptrs_ok({h, w}) || !tokens_ok({target}, 8)) return POETX_EINVAL;
-  v = vocab_sizes(D, T, op);
+  v = vocab_within(D, T, op, ws_bytes);
   if (ldw > kVocabStride || !v.fits) return POETX_EUNSUPPORTED;
-  Carve size(nullptr);
-  carve_vocab(v, size);
-  if (const int e = ws_ok(ws, ws_bytes, size.off)) return e;
+  if (const int e = ws_ok(ws, ws_bytes, vocab_bytes(v))) return e;
   Carve c(ws);
   carve_vocab(v, c);
   v.h = h;
@@ -284,10 +312,7 @@ int poetx_linear_i8_prepare(int64_t m, int64_t n, const int8_t* w0, int8_t* wt, 
 
 size_t poetx_vocab_ws_bytes(const poetx_vocab* D, int64_t T, int op) {
   if (!vocab_ok(D, T) || (op != POETX_OP_VOCAB_FORWARD && op != POETX_OP_VOCAB_BACKWARD)) return 0;
-  VocabDesc v = vocab_sizes(D, T, op);
-  Carve c(nullptr);
-  carve_vocab(v, c);
-  return c.off;
+  return vocab_bytes(vocab_sizes(D, T, op, piece_of(D, T), false));
 }
 
 int poetx_vocab_loss_forward(const poetx_vocab* D, int64_t T, const void* h, int64_t ldh, const void* w, int64_t ldw,

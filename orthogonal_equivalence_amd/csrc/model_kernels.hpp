@@ -107,8 +107,9 @@ struct VocabDesc {
   void* dh = nullptr;
   void* dw = nullptr;
 };
-// Sets the tiles, splits and `fits` from the sizes.
-void vocab_plan(VocabDesc& d);
+// Sets the tiles, splits and `fits` from the sizes; `lean`: the widest column tiles
+// (the fewest pairs) and no splits.
+void vocab_plan(VocabDesc& d, bool lean);
 void vocab_forward(const VocabDesc& d, hipStream_t stream);
 void vocab_backward(const VocabDesc& d, hipStream_t stream);
 

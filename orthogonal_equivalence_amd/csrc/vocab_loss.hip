@@ -702,7 +702,7 @@ TileArgs tile_args(const VocabDesc& D) {
 // us, 580 unsplit; backward of 600 tokens 2.13 ms, 2.70; d = 1024, V = 32000, 64
 // tokens: backward 67 us, 171; T = 65536, d = 512, V = 100: dw split, backward
 // 195 us, 422). Tiles that fill the CUs a few times over are not split.
-KPlan k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
+KPlan k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192, int most_splits) {
   const TileCost* costs = bf16 ? kTileCosts : kTileCostsF32;
   const int kinds = bf16 ? static_cast<int>(kTileKinds) : static_cast<int>(kTileKindsF32);
   const int steps = static_cast<int>((K + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32));
@@ -712,7 +712,7 @@ KPlan k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
     if (bf16 && no_192 && t == kTile192x256) continue;
     const int64_t n = ((M + costs[t].bm - 1) / costs[t].bm) * ((N + costs[t].bn - 1) / costs[t].bn);
     const double step = costs[t].us / (bf16 ? 32 : 1);
-    for (int s = 1; s <= 16 && (s == 1 || (steps >= 8 * s && n * s <= 4 * costs[t].slots)); ++s) {
+    for (int s = 1; s <= most_splits && (s == 1 || (steps >= 8 * s && n * s <= 4 * costs[t].slots)); ++s) {
       double us = static_cast<double>((n * s + costs[t].slots - 1) / costs[t].slots) *
                   static_cast<double>((steps + s - 1) / s) * step;
       if (s > 1) us += 4.0 + static_cast<double>(M) * static_cast<double>(N) * 8.0 * s / 4e6;
@@ -728,17 +728,20 @@ KPlan k_plan(int64_t M, int64_t N, int64_t K, bool bf16, bool no_192) {
 
 }  // namespace
 
-void vocab_plan(VocabDesc& D) {
+void vocab_plan(VocabDesc& D, bool lean) {
   const TileCost* t = D.bf16 ? kTileCosts : kTileCostsF32;
   auto fits = [&](int tile, int64_t M, int64_t N) { D.fits = D.fits && tiles_fit(t[tile], M, N); };
   D.fits = true;
-  D.stat_tile = pick(D.T, D.V, D.bf16);
+  D.stat_tile = !lean    ? pick(D.T, D.V, D.bf16)
+                : D.bf16 ? kTile128x256 + pick_tile(kTileCosts + kTile128x256, kTileKinds - kTile128x256, D.T, D.V)
+                         : kTileF128;
   D.stat_tiles = tiles(D.V, t[D.stat_tile].bn);
   fits(D.stat_tile, D.T, D.V);  // the backward refuses what the forward does
   if (!D.backward) return;
   const int64_t most = std::min(D.V, D.piece), last = D.V % D.piece;
-  D.dh_plan = k_plan(D.T, D.d, most, D.bf16, false);
-  D.dw_plan = k_plan(most, D.d, D.T, D.bf16, true);
+  const int splits = lean ? 1 : 16;
+  D.dh_plan = k_plan(D.T, D.d, most, D.bf16, false, splits);
+  D.dw_plan = k_plan(most, D.d, D.T, D.bf16, true, splits);
   fits(pick(D.T, most, D.bf16), D.T, most);
   if (last) fits(pick(D.T, last, D.bf16), D.T, last);
   fits(D.dh_plan.tile, D.T, D.d * D.dh_plan.splits);
