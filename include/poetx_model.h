@@ -127,7 +127,9 @@ typedef struct poetx_vocab {
   int32_t dtype;  /* POETX_BF16 or POETX_F32 */
   int32_t piece;  /* vocabulary rows whose gradients the backward holds at a time
                    * (rounded up to a multiple of 256); 0 = chosen for the token
-                   * count so that a piece holds 256 MB or the vocabulary */
+                   * count so that a piece holds 256 MB or the vocabulary, and
+                   * at least 1024 rows (2048 T bytes in bfloat16, 4096 T in float:
+                   * more than 256 MB past 131072 or 65536 tokens) */
 } poetx_vocab;
 
 enum { POETX_OP_VOCAB_FORWARD = 0, POETX_OP_VOCAB_BACKWARD = 1 };

@@ -72,3 +72,17 @@ def test_too_little_is_refused(op, piece):
     assert least <= high <= have
     for size in range(0, have, max(1, have // 97)):
         assert enough(D, T, op, size) == (size >= high)
+
+
+@pytest.mark.parametrize("T", [131072, 131073, 400000, 1 << 20, 1 << 24])
+@pytest.mark.parametrize("dtype,es", [("bf16", 2), ("f32", 4)])
+def test_a_piece_of_very_many_tokens_holds_1024_words(T, dtype, es):
+    """As documented: 256 MB a piece, but 1024 words where they take more (less up
+    to a tenth where the pieces are evened out); beside it the gathered rows, dh's
+    float sums, five values a token, and dw's sums where they are split."""
+    d, V = 512, 32000
+    size = mo.poetx_vocab_ws_bytes(mo.make_vocab(d, V, dtype), T, mo.POETX_OP_VOCAB_BACKWARD)
+    parts = T * d * (es + 4) + 20 * T
+    assert max(1 << 28, T * 1024 * es) * 0.9 + parts <= size <= max(1 << 28, T * 1024 * es) + parts + (1 << 28)
+    asked = mo.poetx_vocab_ws_bytes(mo.make_vocab(d, V, dtype, 256), T, mo.POETX_OP_VOCAB_BACKWARD)
+    assert T * 256 * es + parts <= asked <= T * 256 * es + parts + (1 << 28)
