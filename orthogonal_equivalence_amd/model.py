@@ -9,6 +9,11 @@ made on another stream has to be ordered before the call by the caller, as
 for any torch operation. Two-dimensional inputs may have any row stride whose
 rows start on 16-byte boundaries; gradients that come in broadcast (expanded)
 are copied out first.
+
+The functions record no graph: gradients come from the ``_backward`` functions.
+While torch records gradients, an input that requires one is refused, as its
+results would silently be cut off from it; call them under ``torch.no_grad()``
+or within a ``torch.autograd.Function``.
 """
 
 import torch
@@ -21,6 +26,13 @@ _DTYPE = {torch.float32: px.POETX_F32, torch.bfloat16: px.POETX_BF16}
 _NAME = {torch.float32: "f32", torch.bfloat16: "bf16"}
 
 
+def _requires_grad(name, t):
+    """Refuses an input that requires a gradient, where torch records them."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name}: {tuple(t.shape)} requires a gradient, and no graph is recorded here: call under "
+                         "torch.no_grad() and take gradients from the _backward functions")
+
+
 def _rows(name, t, shape, dtype, device):
     """Checks a two-dimensional tensor with contiguous rows; its row stride."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
@@ -30,6 +42,8 @@ def _rows(name, t, shape, dtype, device):
 
 
 def _stride(name, t, shape):
+    if t.requires_grad:
+        _requires_grad(name, t)
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row are not contiguous (strides {s0}, {s1})")
@@ -41,6 +55,8 @@ def _flat(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}, expected contiguous "
                          f"{tuple(shape)} {dtype} on {device}")
+    if t.requires_grad:
+        _requires_grad(name, t)
 
 
 def _first(name, t):
