@@ -71,7 +71,8 @@ def _first(name, t):
 
 def _grad(t):
     """A gradient with rows of its own (autograd hands out broadcast ones)."""
-    return t.contiguous() if 0 in t.stride() or t.stride(-1) != 1 else t
+    s = t.stride()
+    return t.contiguous() if s and (0 in s or s[-1] != 1) else t  # (a scalar is refused with its shape)
 
 
 def _ptr(t):
