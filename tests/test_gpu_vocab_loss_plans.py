@@ -131,3 +131,75 @@ def test_the_workspace_of_more_tokens_serves_fewer():
     # both are within the bound of the same gradients
     _near("dh", dh, f64(want[0]), 2 * np.sqrt(2.0 / 3.0) * U16)
     _near("dw", dw, f64(want[1]), 2 * np.sqrt(2.0 / 3.0) * U16)
+
+
+# rows, columns, workgroups at a time and cost of a round of the bfloat16 tiles, as the launcher has them
+TILES = [(64, 64, 256, 11.2), (64, 64, 512, 16.8), (128, 128, 256, 22.0), (128, 256, 256, 35.0), (192, 256, 256, 46.5),
+         (256, 256, 256, 57.0)]
+
+
+def _k_plan(rows, cols, k, without=None):
+    """Tile and splits of a bfloat16 product, by the launcher's rule."""
+    steps, best, least = -(-k // 64), None, np.inf
+    for i, (bm, bn, slots, us) in enumerate(TILES):
+        if i == without:
+            continue
+        n = -(-rows // bm) * -(-cols // bn)
+        for s in range(1, 17):
+            if s > 1 and (steps < 8 * s or n * s > 4 * slots):
+                break
+            cost = -(-n * s // slots) * -(-steps // s) * us / 32
+            cost += 4.0 + rows * cols * 8.0 * s / 4e6 if s > 1 else 0.0
+            if cost < least:
+                least, best = cost, (i, s)
+    return best
+
+
+# dh in every wide tile (its index in TILES) with a split of its sum over the
+# vocabulary, with all and with some of the tokens counted, in one piece and in
+# several whose sums add up
+@pytest.mark.parametrize("ignored", [0.0, 0.6])
+@pytest.mark.parametrize("T,d,V,piece,plan", [(1000, 1536, 6000, 0, (3, 5)), (1500, 1536, 12000, 0, (4, 5)),
+                                              (1200, 2504, 8000, 0, (5, 5)), (1000, 2504, 9000, 4096, (3, 3)),
+                                              (1200, 2048, 16100, 8192, (3, 3)), (1200, 2504, 16384, 8192, (5, 5))])
+def test_wide_tiles_with_a_split_sum(T, d, V, piece, plan, ignored):
+    words = min(piece or V, V)
+    assert _k_plan(T, d, words) == plan
+    # the library's splits show in the size of its sums
+    splits_w = _k_plan(words, d, T, without=4)[1]
+    sums = 4 * d * (plan[1] * T + (splits_w * words if splits_w > 1 else 0))
+    size = mo.poetx_vocab_ws_bytes(mo.make_vocab(d, V, "bf16", piece), T, mo.POETX_OP_VOCAB_BACKWARD)
+    rest = size - sums - 2 * T * (-(-words // 256) * 256 + -(-d // 64) * 64)
+    assert 0 < rest < 64 * T
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V} piece={piece} ignored={ignored}", flush=True)
+    rng = np.random.default_rng([T, d, V, int(10 * ignored)])
+    h, w, t = _inputs(rng, T, d, V, "bf16", ignored)
+    LOSS, LSE, DH, DW = _want(h, w, t)
+    loss, lse = model.vocab_loss(h, w, t, piece)
+    dh, dw = model.vocab_loss_backward(h, w, t, lse, piece=piece)
+    torch.cuda.synchronize()
+    bound = _bound(h, w, "bf16")
+    _near("loss", loss, LOSS, 1e-4)
+    _near("lse", lse, LSE, 1e-4)
+    _near("dh", dh, DH, bound)
+    _near("dw", dw, DW, bound)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,counted", [(255, 264, 3001, 255), (600, 136, 500, 255), (260, 512, 2000, 255),
+                                           (700, 128, 5000, 510)])
+def test_errors_of_whole_matrices(T, d, V, counted, act):
+    """The mean loss over 255 or 510 tokens: 1 / 255 lies almost half a step of
+    bfloat16 from its neighbours, so that a factor rounded into the targets'
+    terms, all alike, is an error of 0.39% by itself, outside the bound."""
+    print(f"\n[gpu] vocab_loss T={T} d={d} V={V} counted={counted} {act}", flush=True)
+    rng = np.random.default_rng([T, counted])
+    h, w, t = _inputs(rng, T, d, V, act, 0.0)
+    t[torch.from_numpy(rng.permutation(T)[counted:]).cuda()] = -100
+    _, _, DH, DW = _want(h, w, t)
+    _, lse = model.vocab_loss(h, w, t)
+    dh, dw = model.vocab_loss_backward(h, w, t, lse)
+    torch.cuda.synchronize()
+    bound = _bound(h, w, act)
+    _near("dh", dh, DH, bound)
+    _near("dw", dw, DW, bound)
