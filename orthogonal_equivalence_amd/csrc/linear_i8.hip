@@ -3,12 +3,14 @@
 // in the epilogue.
 //
 // Many tokens are bound by the matrix cores and by the LDS that feeds them
-// (tile_gemm.hpp): T = 8192, m = 4096, n = 14336 in 388 us, 2.48 POP/s, where the
+// (tile_gemm.hpp): T = 8192, m = 4096, n = 14336 in 390 us, 2.47 POP/s, where the
 // library's plain product reaches 2.1 to 2.3. In between, the K loop of a tile
-// is a chain of latencies, which smaller tiles spread over more CUs (T = 777, m =
-// 2064, n = 5136: 22 us, 147 tiles of 128 x 256; 192 x 128 would take 20 us there
-// and lose at every other of 14 sizes tried). Few tokens are bound by the n m bytes of
-// the weight (k_linear_i8_few: T = 1, m = 4096, n = 14336 10.4 us, 5.6 TB/s).
+// is a chain of latencies that no other workgroup shares (T = 777, m = 2064, n =
+// 5136: 22 us, 147 tiles of 128 x 256 on 256 CUs; 192 x 128 would take 20 us there
+// and lose at every other of 14 sizes tried; T = 96, m = 13824, n = 5120: 32 us for
+// 14 us of bytes). Few tokens are bound by the n m bytes of the weight
+// (k_linear_i8_few: T = 1, m = 4096, n = 14336 11 us, 5.3 TB/s, with the weight in
+// the last-level cache, and 14.3 us, 4.1 TB/s, from memory).
 #include "model_kernels.hpp"
 #include "tile_gemm.hpp"
 
@@ -59,7 +61,8 @@ void launch_tail(const I8Args& a, bool bf16, hipStream_t st) {
 
 // Up to 32 TT tokens: a workgroup computes 32 OB outputs, its NW waves taking
 // 128-byte pieces of K in turn (a row's next NW pieces are read at the same
-// time). Bound by the weight's bytes, which are read once. A wave streams its
+// time). Bound by the weight's bytes, which are read once (58.9 MB with the codes
+// at T = 1, 4096 x 14336, for 58.7 of weight). A wave streams its
 // pieces of weights and codes through an LDS ring of its own, D pieces deep, with
 // direct loads of whole 128-byte lines, and waits for nothing but its own loads:
 // no barrier until the waves' sums are joined.
@@ -183,10 +186,11 @@ bool linear_i8(const LinearI8Desc& d, hipStream_t st) {
   const I8Args a{{d.xq, d.m, d.T, d.m}, {d.wt, d.m, d.n, d.m}, d.xs, d.ws, d.z, d.ldz,
                  static_cast<int>(d.T), static_cast<int>(d.n), static_cast<int>(d.m)};
   // Few tokens: one ring a wave. 64 outputs a workgroup where 32 would make
-  // more than one round over the 256 CUs (measured at T = 1: m = 4096, n =
-  // 14336 10.4 us against 14.8; m = 13824, n = 5120 13.7 against 12.1).
-  // 33 to 64 tokens with that many outputs go to the tiles (T = 64, same
-  // shapes: 12.5 us against 20.1; 22.8 against 18.8).
+  // more than one round over the 256 CUs (64 outputs against 32 at T = 1, weight in
+  // the cache: m = 4096, n = 14336 11.1 us, 14.3; m = 13824, n = 5120 14.8, 12.4; not
+  // in the cache: 14.4, 14.6; 22.8, 15.6). 33 to 64 tokens with that many outputs go
+  // to the tiles (T = 64, tiles against rings, same shapes: in the cache 13.2 us, 19.3;
+  // 26.4, 18.8; not in it 16.5, 21.4; 36.7, 27.7).
   if (a.T <= 32) {
     if (a.n > 256 * 32) launch_few<2, 1, 4, 2>(a, d.out_bf16, st);
     else launch_few<1, 1, 4, 4>(a, d.out_bf16, st);

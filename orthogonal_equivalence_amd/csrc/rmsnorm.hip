@@ -5,9 +5,12 @@
 // All of it is bound by HBM: a row is read once, held in registers as float
 // across its reductions and written once. A row belongs to TPR threads (from 8
 // to sixteen waves), each with CH chunks of 8 consecutive features, 16 bytes of
-// bfloat16 a load; rows too wide for that are read again per pass. Measured in
+// bfloat16 a load; rows too wide for that are read again per pass. (The backward of
+// rows of 8200 to 24576 features needs more than its 128 registers a thread: 25 to 379
+// lie in scratch memory, and T = 4096, n = 13824 takes 216 us for 89 us of bytes.)
+// Measured in
 // bfloat16 with the residual (a large copy reaches 5.1 TB/s, more where the
-// last-level cache holds the data): T = 8192, n = 4096 forward 44 us (6.1
+// last-level cache holds the data): T = 8192, n = 4096 forward 41 us (6.5
 // TB/s), int8 rows 39 us, backward 42 us and 5 us for dgain; T = 4096, n =
 // 5120 forward 31 us, backward 31 us; one row of 4096 3.5 us.
 #include "common.hpp"

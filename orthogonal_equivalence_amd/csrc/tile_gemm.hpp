@@ -46,7 +46,7 @@ typedef unsigned int tg_u32x4_t __attribute__((ext_vector_type(4)));
 
 // Tiles of a product: it takes the one whose rounds over the CUs cost least. A
 // round's time, measured with every slot taken, in us; it grows with K alike
-// for all. 1- and 2-byte products, as the int8 product at 32 K steps (m =
+// for all (but for the first loads and the epilogue, a larger share of a short K). 1- and 2-byte products, as the int8 product at 32 K steps (m =
 // 4096): small tiles are chains of latencies, and more of them at once hide
 // each other's (64 x 64 over two groups of waves, or two workgroups a CU).
 enum TileKind { kTile64x2, kTile64, kTile128, kTile128x256, kTile192x256, kTile256, kTileKinds };

@@ -20,7 +20,7 @@
 // 1.33 PFLOP/s, where the library's plain products of these shapes reach 1.47 to
 // 1.57. Few tokens are bound by the bytes of w and dw (d = 4096, V = 131072, T =
 // 64: forward 0.21 ms for 1.07 GB, backward 0.80 ms for 3.2), small calls by the
-// latency of seven launches.
+// latency of six launches.
 #include "model_kernels.hpp"
 #include "tile_gemm.hpp"
 
@@ -94,9 +94,10 @@ __global__ void __launch_bounds__(1024) k_vocab_count(const RowsArgs a) {
 // not counted gets zeros in its row of dh. A workgroup does `per` tokens, 64 at
 // a time, and finds its first compact row by counting the targets before its
 // own, all workgroups at the same time; with CHUNKS, from the counts of
-// k_vocab_count, those of its own chunk only. Bound by the rows' bytes, read and
-// written once (T = 4096, d = 4096: 67 MB in 23 us, 6 of them before the first
-// row).
+// k_vocab_count, those of its own chunk only. The rows' bytes, read and written
+// once, take half of its time (T = 4096, d = 4096: 67 MB in 25 to 30 us, 13 at a
+// copy's rate): 6 us pass before the first row, and the compiler keeps the eight
+// loads that a lane has in flight in scratch memory, 144 bytes a lane.
 template <int NW, bool CHUNKS>
 __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int per) {
   __shared__ int red[2][NW];
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
       if (to >= 0) {
         const uint4* src = a.h + (b + i) * a.ldh;
         uint4* dst = a.hc + to * a.ldhc;
-        for (int c = lane; c < a.chunks; c += 512) {  // 8 KB in flight a wave
+        for (int c = lane; c < a.chunks; c += 512) {  // 8 KB a wave at a time
           uint4 v[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u)
@@ -260,7 +261,8 @@ struct Turned<WideTiles<true, false, false>> {
 
 // Which of them for the counted rows, whose number the host does not know: the
 // cheapest whose tiles fit the launch (T = 1111 of which 555 count, d = 2056, V
-// = 50021: forward 157 us with three rounds of 192 rows, 171 with three of 256).
+// = 50021, this product: 143 us with three rounds of 192 rows and 166 with three of
+// 256 where w is in the last-level cache, 178 and 185 where it is not).
 __device__ __forceinline__ int pick_wide(int rows, int tiles_n, int most) {
   int best = kTile256;
   float least = INFINITY;
@@ -674,10 +676,11 @@ void gather_rows(const VocabDesc& D, bool backward, hipStream_t st) {
   const RowsArgs a{D.target, D.V, T, D.rows, backward ? D.lse_in : nullptr, D.dloss, D.scale,
                    static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc), D.ldhc * es / 16,
                    static_cast<uint4*>(backward ? D.dh : nullptr), static_cast<int>(D.d * es / 16)};
-  // a row a wave; few tokens on as many CUs as they have fours (d = 4096, NW = 4
-  // against 16: T = 1111 9.2 us, 11.3; 4096 28 us, 23; 8192 62 us, 48); every
-  // workgroup reads all targets where that costs less than a launch of counts (T =
-  // 8192: 48 us against 45 + 5; T = 65536, d = 512: 107 us against 34 + 5)
+  // a row a wave; few tokens on as many CUs as they have fours (d = 4096, h not in
+  // the cache, NW = 4 against 16: T = 1111 13.8 us, 16.5; 2048 15.5, 16.6; 4096
+  // 28.6, 26.2; 8192 64.8, 53.5); every workgroup reads all targets where that costs
+  // no more than a launch of counts (T = 8192: 53.5 us against 49.5 + 5.4; T = 65536,
+  // d = 512: 229 us against 40.8 + 5.2)
   if (T <= 2048) {
     hipLaunchKernelGGL((k_vocab_gather<4, false>), dim3(tiles(T, 4)), dim3(256), 0, st, a, 4);
   } else if (T <= 2 * kVocabChunk) {
