@@ -289,9 +289,11 @@ __device__ __forceinline__ bool vocab_place(int bid, int count, int tiles_n, int
   return true;
 }
 
-// exp(x) of a logit against a reference, both times log2(e)
-__device__ __forceinline__ float exp_rel(float l, float ref2) {
-  return __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -ref2));
+// exp(l - ref). The difference is taken first, exact where the two are near: as one
+// fused step against ref in powers of two (no faster, the products bound these
+// kernels) its rounding, 1e-5 at logits of 200, would be in every term.
+__device__ __forceinline__ float exp_rel(float l, float ref) {
+  return __builtin_amdgcn_exp2f((l - ref) * kLog2e);
 }
 
 // Joins (m, s) with (m2, s2): sums of exp(x - m) over disjoint sets whose largest
@@ -299,7 +301,7 @@ __device__ __forceinline__ float exp_rel(float l, float ref2) {
 __device__ __forceinline__ void join_stat(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
   const float ref = top == -INFINITY ? 0.f : top;
-  s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - ref) * kLog2e);
+  s = s * exp_rel(m, ref) + s2 * exp_rel(m2, ref);
   // a NaN logit leaves its mark in the sum; fmaxf drops it
   m = top;
 }
@@ -322,9 +324,7 @@ __device__ __forceinline__ void mask_columns(f32x4_t (&acc)[Cfg::TM][Cfg::TN], i
 // Maximum and sum of every row over the tile's columns, and the targets' logits.
 // The exponentials come from the sums as they lie in the registers (T = 8192, d
 // = 4096, V = 131072: 6.4 ms, 1.38 PFLOP/s, matrix cores busy in 72% of the
-// cycles), one fused step each against the maximum in powers of two. What that
-// reference's rounding puts on all of them alike (1e-5 of them at logits of 200)
-// is taken out of their sum.
+// cycles).
 template <class Cfg>
 __device__ __forceinline__ void stat_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
@@ -359,16 +359,13 @@ __device__ __forceinline__ void stat_tile(const TileArgs& a, int bid, int count,
         for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      const bool none = m == -INFINITY;
-      const float ref = none ? 0.f : m * kLog2e, ref_off = none ? 0.f : fmaf(m, kLog2e, -ref);
+      const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) s += exp_rel(acc[i][j][r], ref);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      s *= __builtin_amdgcn_exp2f(-ref_off);
-      if (!none && s < 1.f) s = 1.f;  // the maximum's own term (a NaN stays)
       if (lane < 16) red[wn * Cfg::BM + row] = make_float2(m, s);
     }
   }
@@ -437,10 +434,8 @@ __global__ void __launch_bounds__(1024) k_vocab_join(const float2* stat, int til
 // of them alike (with g = 1 / count in bfloat16, 0.3% of dh and dw in place of
 // 0.17%). p [count][ldp], zero in the columns past the vocabulary.
 //
-// The probabilities are exponentials against lse in powers of two, whose rounding
-// (1e-5 of them at an lse of 200) is taken out through g, one factor a row. The
-// target's p - 1 is then off by the float lse's own half step; where that takes
-// it past 0, it is 0, as p is at most 1.
+// The probabilities are off by the float lse's own half step (8e-6 of them at an lse
+// of 200). Where that takes the target's p - 1 past 0, it is 0, as p is at most 1.
 template <class Cfg>
 __device__ __forceinline__ void dlogits_tile(const TileArgs& a, int bid, int count, char* smem) {
   int tm, tn;
@@ -459,12 +454,11 @@ __device__ __forceinline__ void dlogits_tile(const TileArgs& a, int bid, int cou
     const bool in = row < count;
     const int at = in ? row : m0;  // rows past the count are not stored
     const int tcol = a.r.tgt[at] - a.v0 - n0;
-    const float lse = a.r.lse[at], ref = lse * kLog2e, ref_off = fmaf(lse, kLog2e, -ref);
-    const float g = a.r.g[at], gp = fabsf(ref) < INFINITY ? g * __builtin_amdgcn_exp2f(-ref_off) : g;
+    const float lse = a.r.lse[at], g = a.r.g[at];
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = gp * exp_rel(acc[i][j][r], ref);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = g * exp_rel(acc[i][j][r], lse);
     if (__any(static_cast<unsigned>(tcol - wn * Cfg::WTN) < Cfg::WTN)) {
 #pragma unroll
       for (int j = 0; j < Cfg::TN; ++j)

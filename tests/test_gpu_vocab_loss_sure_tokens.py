@@ -4,9 +4,8 @@ small number beside large logits, and never negative.
 Every logit here is one product of two bfloat16 values (the other features of a
 row are zero) and exact in float32, so that only the softmax's own roundings
 count. Bounds in units of u32, each step's rounding in its order: a tile's sum
-of exponentials holds the exponential of its maximum (1 ulp, 2 u32, each for it
-and for the factor that takes out its reference's rounding, 1 for their
-product), its logarithm 1 ulp of the result or of the argument near 1 (4). Terms
+of exponentials holds the exponential of its maximum (5 at most, none where the
+difference is taken first), its logarithm 1 ulp of the result or of the argument near 1 (4). Terms
 beside the maximum are off by their exponent's size, at most 36, plus the sums'
 and the difference's roundings, all relative to terms that are at most the loss
 itself.
@@ -112,3 +111,32 @@ def test_infinities_in_the_vocabulary_stay_as_the_formula_has_them(act):
     within("loss", loss[:2], np.array([want, want]), 200 * U32)
     within("lse", lse[:2], np.array([want - 1.0, want - 2.0]), 200 * U32)
     assert not torch.isfinite(loss[2]) and not torch.isfinite(lse[2])
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("at", ["largest", "other"])
+def test_logits_of_any_size(at, act):
+    """Logits from 2^31 to 2^90, whose steps in float32 are themselves large: the
+    loss is the difference to the largest, rounded once, and 0 for the largest;
+    a sure token's gradient is 0, a wrong one's -g at the target and g at the
+    largest."""
+    rng = np.random.default_rng(8)
+    T, V, d = 60, 700, 72
+    h, w = torch.zeros(T, d), torch.zeros(V, d)
+    h[:, 0] = _bf16(rng.uniform(1.0, 2.0, T)) * 2.0 ** torch.linspace(31, 90, T).round()
+    h[range(T), range(8, 8 + T)] = 1.0
+    w[:, 0] = _bf16(rng.uniform(-1.0, 0.0, V))
+    w[411, 0] = 1.25
+    t = torch.full((T,), 411 if at == "largest" else 17, dtype=torch.int64, device="cuda")
+    h, w = h.to(DTYPES[act]).cuda(), w.to(DTYPES[act]).cuda()
+    loss, lse = model.vocab_loss(h, w, t)
+    _, dw = model.vocab_loss_backward(h, w, t, lse, torch.ones(T, device="cuda"))
+    torch.cuda.synchronize()
+    L = f64(h)[:, 0] * 1.25
+    within("lse", lse, L, U32 * L)
+    within("loss", loss, L - f64(h)[:, 0] * f64(w)[int(t[0]), 0], 2 * U32 * L if at == "other" else 0.0)
+    dl = f64(dw)[:, 8:8 + T]
+    want = np.zeros((V, T))
+    if at == "other":
+        want[411], want[17] = 1.0, -1.0
+    assert np.array_equal(dl, want)
