@@ -70,7 +70,6 @@ int norm_common(int64_t T, int64_t n, int dtype, const void* x, int64_t ldx, con
 constexpr int64_t kVocabTokens = int64_t(1) << 24;
 constexpr int64_t kPieceBytes = int64_t(1) << 28;
 constexpr int64_t kPieceMax = int64_t(1) << 20;
-constexpr int64_t kVocabStride = int64_t(1) << 22;  // a tile's offsets stay below 2^31 bytes
 
 bool vocab_ok(const poetx_vocab* D, int64_t T) {
   return D && D->d >= 8 && D->d <= (int64_t(1) << 17) && D->d % 8 == 0 && D->V >= 1 && D->V <= kMaxWidth &&

@@ -63,6 +63,9 @@ bool linear_i8(const LinearI8Desc& d, hipStream_t stream);
 // in [0, V)) are gathered to the front: compact row c is token idx[c], and
 // pos[t] is token t's compact row or -1.
 constexpr int kVocabChunk = 4096;
+// Elements from row to row of what a product reads in its place: the offsets of a
+// tile's rows (256 of bfloat16, 128 of float) stay below 2^31 bytes.
+constexpr int64_t kVocabStride = int64_t(1) << 22;
 struct VocabRows {
   int2* chunk;     // [T / kVocabChunk, rounded up] counted tokens and largest gradient (more than two chunks)
   int32_t* pos;    // [T]

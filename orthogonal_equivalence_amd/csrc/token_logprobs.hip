@@ -738,7 +738,8 @@ void token_forward(const VocabDesc& D, hipStream_t st) {
   // Where all rows' tiles are one round, fewer rows cost as much: they stay in their
   // places, and the launch that gathers the counted ones, 5 us, is saved.
   const bool one_round = chunk >= D.T && pick_count(t, D.T, D.V, D.bf16) <= 256;
-  if (D.target && !one_round) {
+  // Rows too far apart for a tile's offsets are gathered, counted or not.
+  if ((D.target && !one_round) || D.ldh > kVocabStride) {
     vocab_gather(D, false, st);
     h = static_cast<const char*>(D.hc);
     ldh = D.ldhc;
