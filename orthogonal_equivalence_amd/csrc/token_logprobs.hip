@@ -90,10 +90,13 @@ __device__ __forceinline__ void join_token(float& m, float& q, float& u, float m
 }
 
 // Two logits' distances below their group's maximum in 16 bits: the upper halves
-// of the (negative) floats, and so no further below than they are, by less than
-// 2^-7 of it.
+// of the (negative) floats next nearer to 0. A difference of two floats may be rounded
+// away from 0 (1e-6 - 100 is -100), by half a step at most: taken one step back, the
+// code is no further below the maximum than the logit is, and nearer by less than 2^-7 +
+// 2^-23 of it. Zeros, infinities and NaN stay.
 __device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
-  return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+  constexpr float kBack = 0x1.fffffep-1f;  // 1 - 2^-24: rounds to the next float towards 0
+  return (__float_as_uint(lo * kBack) >> 16) | (__float_as_uint(hi * kBack) & 0xffff0000u);
 }
 // 32 columns lie as four lanes hold them, eight codes each: the column of code p,
 // and the code of a column.
@@ -340,7 +343,9 @@ __device__ __forceinline__ RowOut row_out(float q, float u) {
 
 // A code's logit, or a little more: its group's maximum and the distance below it
 // (that of a NaN is not negative; beside an infinite maximum it is infinite itself).
-// `share`: 1, or 1 + 2^-7 for a key that the logit is not below.
+// `share`: 1, or kShare for a key that the logit is not below. The sum is of floats
+// that the logit, a float itself, lies between, and so does its rounding.
+constexpr float kShare = 1.f + 0x1p-7f + 0x1p-15f;  // times 8 bits exact
 __device__ __forceinline__ uint32_t code_key(float most, uint32_t code, float share = 1.f) {
   const float d = __uint_as_float(code << 16) * share;
   const float base = most == -INFINITY ? 0.f : fminf(most, kFloatMax);
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 4 : 6) k_token_select(const T
   if (fine) {
     for (int i = tid; i < G << shift; i += NT)
       codes_of(i >> shift, (i & ((1 << shift) - 1)) * 8, [&](int col, float top, uint32_t code) {
-        atomicMax(&keys[col & (kSlots - 1)], code_key(top, code, 1.0078125f));
+        atomicMax(&keys[col & (kSlots - 1)], code_key(top, code, kShare));
       });
   } else {
     all_groups([&](int g, uint32_t key) { atomicMax(&keys[g & (kSlots - 1)], key); });
@@ -504,7 +509,6 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 4 : 6) k_token_select(const T
       const int n = __popcll(__ballot(v.x >= next)) + __popcll(__ballot(v.y >= next));
       tau = n >= K ? next : tau;
     }
-    tau = max(tau, 2u) - 2;  // less what the sum of a maximum and a distance rounds
   }
   if (!fine)
     all_groups([&](int g, uint32_t key) {
