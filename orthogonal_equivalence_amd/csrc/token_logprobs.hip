@@ -237,15 +237,14 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 
 struct SelectLds {
   int hist[256];
-  int sums[16];
+  int sums[2][16];
   uint32_t prefix;
   int need;
 };
 
-// The K largest of n > K keys, equal ones by the lowest index: put(slot, i) for
-// each, slots in the order of the indexes. Eight bits of the K-th key a pass.
-template <int NT, class Key, class Put>
-__device__ __forceinline__ void select_largest(int n, int K, SelectLds& s, Key&& key, Put&& put) {
+// The K-th largest of n >= K keys, eight bits of it a pass.
+template <int NT, class Key>
+__device__ __forceinline__ uint32_t kth_largest(int n, int K, SelectLds& s, Key&& key) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t prefix = 0, mask = 0;
   int need = K;  // of the keys that share the prefix
@@ -283,35 +282,41 @@ __device__ __forceinline__ void select_largest(int n, int K, SelectLds& s, Key&&
     need = s.need;
     mask |= 255u << shift;
   }
-  // all above the K-th key, and the first `need` of those equal to it
-  int equal = 0, slot = 0;  // before this round of NT keys
+  return prefix;
+}
+
+// Of the columns 0 .. n - 1 those of kind 2, and the first `most` of kind 1, numbered in
+// their order: put(number, column). Returns how many there are.
+template <int NT, class Kind, class Put>
+__device__ __forceinline__ int number_columns(int n, int most, SelectLds& s, Kind&& kind, Put&& put) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const unsigned long long below = (1ull << lane) - 1;
+  int alike = 0, all = 0;  // before this round of NT columns
   for (int i0 = 0; i0 < n; i0 += NT) {
-    const uint32_t k = i0 + tid < n ? key(i0 + tid) : 0;
-    const bool in = i0 + tid < n;
-    const unsigned long long below = (1ull << lane) - 1;
-    const unsigned long long eq = __ballot(in && k == prefix);
-    if (lane == 0) s.sums[wave] = __popcll(eq);
+    const int k = i0 + tid < n ? kind(i0 + tid) : 0;
+    const unsigned long long one = __ballot(k == 1);
+    if (lane == 0) s.sums[0][wave] = __popcll(one);
     __syncthreads();
-    int rank = equal + __popcll(eq & below);
+    int rank = alike + __popcll(one & below);
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
-      rank += w < wave ? s.sums[w] : 0;
-      equal += s.sums[w];
+      rank += w < wave ? s.sums[0][w] : 0;
+      alike += s.sums[0][w];
     }
-    const bool take = in && (k > prefix || (k == prefix && rank < need));
-    const unsigned long long all = __ballot(take);
+    const bool take = k == 2 || (k == 1 && rank < most);
+    const unsigned long long in = __ballot(take);
+    if (lane == 0) s.sums[1][wave] = __popcll(in);
     __syncthreads();
-    if (lane == 0) s.sums[wave] = __popcll(all);
-    __syncthreads();
-    int to = slot + __popcll(all & below);
+    int to = all + __popcll(in & below);
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
-      to += w < wave ? s.sums[w] : 0;
-      slot += s.sums[w];
+      to += w < wave ? s.sums[1][w] : 0;
+      all += s.sums[1][w];
     }
     if (take) put(to, i0 + tid);
-    __syncthreads();
   }
+  __syncthreads();
+  return all;
 }
 
 // products exact (bfloat16's in float), their sum in double
@@ -358,9 +363,14 @@ __device__ __forceinline__ uint32_t code_key(float most, uint32_t code, float sh
 // maxima. The maxima fall into 128 slots; the K-th largest slot, found bit by bit by
 // counting, is a lower bound of the K-th largest logit, and what reaches it, a few
 // more than K, are the candidates: their logits are formed again in double, which
-// float's rounding does not order, and ranked. Where too much reaches it (many equal
-// logits), the candidates are the kCandidates largest codes, found digit by digit,
-// equal ones by the lowest index.
+// float's rounding does not order, and ranked.
+//
+// Where more than kCandidates reach it, the bound is the K-th largest of the codes' own
+// lower bounds, found digit by digit. It is no less than the K-th largest maximum: what
+// reaches it lies in the fewer than K groups with a larger one, under 64 K codes (of a
+// group with a logit far above the others all may reach it), which are taken kCandidates
+// at a time, with the best of those before. Or its float logit is the bound itself: of
+// these the kCandidates of the lowest index are taken.
 constexpr int kSlots = 128, kGroupList = 256, kCandidates = 512;
 
 // v op'd over the wave, in every lane; op commutes. Within rows of 16 lanes by moves
@@ -526,55 +536,102 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 4 : 6) k_token_select(const T
         if (at < kCandidates) ids[at] = col;
       });
   __syncthreads();
-  int n = counts[1];
-  if ((!fine && ng > kGroupList) || n > kCandidates) {
-    n = kCandidates;  // of more words than that
-    select_largest<NT>(
-        a.V, n, s,
-        [&](int i) {
-          const int g = i / a.group;
-          return code_key(most_of(g), codes[g * a.group + column_code(i % a.group)]);
-        },
-        [&](int to, int i) { ids[to] = i; });
-  }
-
-  // two candidates a wave at a time, up to 8 or 4 KB of each in flight: few rows are bound by
-  // latency, many by bandwidth (T = 8192, V = 131072: 5.4 TB/s of w's rows)
-  const uint4* const from = chunks <= HROW ? hrow : h;
-  for (int k = wave; k < n; k += 2 * NW) {
-    const int k2 = k + NW < n ? k + NW : k;
-    const uint4* const w0 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + ids[k] * a.ldw);
-    const uint4* const w1 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + ids[k2] * a.ldw);
-    double v0 = 0, v1 = 0;
-    int i = lane;
-    auto step = [&](auto batch) {
-      constexpr int B = decltype(batch)::value;
-      for (; i + (B - 1) * 64 < chunks; i += B * 64) {
-        uint4 y0[B], y1[B];
-#pragma unroll
-        for (int q = 0; q < B; ++q) {
-          y0[q] = w0[i + q * 64];
-          y1[q] = w1[i + q * 64];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int q = 0; q < B; ++q) {
-          const uint4 z = from[i + q * 64];
-          v0 = dot16(z, y0[q], v0, T{});
-          v1 = dot16(z, y1[q], v1, T{});
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    };
-    step(std::integral_constant<int, NT == 1024 ? 8 : 4>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 1>{});
-    v0 = sum_wave(v0);
-    v1 = sum_wave(v1);
-    if (lane == 0) {
-      exact[k] = v0;
-      exact[k2] = v1;
+  int n = counts[1], kept = 0;
+  const bool many = (!fine && ng > kGroupList) || n > kCandidates;
+  auto key_of = [&](int i, float share) {
+    const int g = i / a.group;
+    return code_key(most_of(g), codes[g * a.group + column_code(i % a.group)], share);
+  };
+  if (many) tau = kth_largest<NT>(a.V, K, s, [&](int i) { return key_of(i, kShare); });
+  // candidate i's rank among n, and the largest logit of them
+  auto rank_of = [&](int i, int n, double& most) {
+    const double v = exact[i], order = v == v ? v : -INFINITY;
+    const int id = ids[i];
+    int rank = 0;
+    most = -INFINITY;
+    for (int k = 0; k < n; ++k) {
+      const double w = exact[k] == exact[k] ? exact[k] : -INFINITY;
+      rank += w > order || (w == order && ids[k] < id);
+      most = w > most ? w : most;
     }
+    return rank;
+  };
+  const uint4* const from = chunks <= HROW ? hrow : h;
+  for (int done = 0;;) {
+    int all = 0;
+    if (many) {
+      const int room = kCandidates - kept;
+      all = number_columns<NT>(
+          a.V, kCandidates, s,
+          [&](int i) {
+            const uint32_t most = key_of(i, 1.f);
+            return most < tau ? 0 : most == tau && key_of(i, kShare) == tau ? 1 : 2;
+          },
+          [&](int at, int i) {
+            if (at >= done && at < done + room) ids[kept + at - done] = i;
+          });
+      n = kept + min(all - done, room);
+      done += room;
+    }
+    // two candidates a wave at a time, up to 8 or 4 KB of each in flight: few rows are bound by
+    // latency, many by bandwidth (T = 8192, V = 131072: 5.4 TB/s of w's rows)
+    for (int k = kept + wave; k < n; k += 2 * NW) {
+      const int k2 = k + NW < n ? k + NW : k;
+      const uint4* const w0 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + ids[k] * a.ldw);
+      const uint4* const w1 = reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + ids[k2] * a.ldw);
+      double v0 = 0, v1 = 0;
+      int i = lane;
+      auto step = [&](auto batch) {
+        constexpr int B = decltype(batch)::value;
+        for (; i + (B - 1) * 64 < chunks; i += B * 64) {
+          uint4 y0[B], y1[B];
+#pragma unroll
+          for (int q = 0; q < B; ++q) {
+            y0[q] = w0[i + q * 64];
+            y1[q] = w1[i + q * 64];
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int q = 0; q < B; ++q) {
+            const uint4 z = from[i + q * 64];
+            v0 = dot16(z, y0[q], v0, T{});
+            v1 = dot16(z, y1[q], v1, T{});
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      };
+      step(std::integral_constant<int, NT == 1024 ? 8 : 4>{});
+      step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 1>{});
+      v0 = sum_wave(v0);
+      v1 = sum_wave(v1);
+      if (lane == 0) {
+        exact[k] = v0;
+        exact[k2] = v1;
+      }
+    }
+    if (!many || done >= all) break;
+    // the best of this batch and of those before, to the front
+    constexpr int OWN = (kCandidates + NT - 1) / NT;
+    __syncthreads();
+    double v[OWN];
+    int id[OWN], rank[OWN];
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+      const int i = min(tid + q * NT, n - 1);
+      v[q] = exact[i];
+      id[q] = ids[i];
+      double most;
+      rank[q] = tid + q * NT < n ? rank_of(i, n, most) : a.top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+      if (rank[q] >= a.top) continue;
+      exact[rank[q]] = v[q];
+      ids[rank[q]] = id[q];
+    }
+    kept = min(n, a.top);
   }
   const float4 part = lane < NW ? red[lane] : make_float4(-INFINITY, -1.f, 0.f, 0.f);
   m = part.x, sum = part.y, u = part.z;
@@ -587,21 +644,14 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 4 : 6) k_token_select(const T
   }
   __syncthreads();
   for (int i = tid; i < n; i += NT) {
-    const double v = exact[i], order = v == v ? v : -INFINITY;
-    const int id = ids[i];
-    int rank = 0;
-    double most = -INFINITY;
-    for (int k = 0; k < n; ++k) {
-      const double w = exact[k] == exact[k] ? exact[k] : -INFINITY;
-      rank += w > order || (w == order && ids[k] < id);
-      most = w > most ? w : most;
-    }
+    double most;
+    const int rank = rank_of(i, n, most);
     if (rank >= a.top) continue;
     const int64_t at = static_cast<int64_t>(t) * a.top + rank;
     // The maximum that log s is taken from is a float sum, off by its rounding; the log of
     // all exponentials is off by the maximum's share of that.
-    const double m64 = m, lp = ((v - m64) + (m64 - most) / (1.0 + sum)) * a.inv_temp - o.log_s;
-    a.top_ids[at] = id;
+    const double m64 = m, lp = ((exact[i] - m64) + (m64 - most) / (1.0 + sum)) * a.inv_temp - o.log_s;
+    a.top_ids[at] = ids[i];
     a.top_logprobs[at] = lp > 0 ? 0.f : static_cast<float>(lp);  // NaN stays
   }
 }
