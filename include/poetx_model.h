@@ -184,9 +184,9 @@ POETX_API int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const v
  *    top = 0. Both go by the logits in double (products of h and w summed in
  *    double), equal ones by the lower index: so the order does not depend on
  *    float32's rounding, or on how many tokens a call holds. What is ordered so is
- *    what float32 logits put among the top + 8 largest, at least; where more than 512
- *    logits reach the last of these (many equal ones), the 512 largest in 16 bits
- *    below the maximum of their 32 or 64 neighbours, equal ones by the lower index.
+ *    what float32 logits put among the top + 8 largest, at least; of logits that are
+ *    equal to the last of these in float32, and with the others are more than 512, the
+ *    512 of the lowest index.
  *  - stat [T][2], 8-byte aligned, for the backward: the row's largest logit before
  *    the temperature, max, and log sum_v exp(l[t][v] - max / temperature), so that lse
  *    = stat[0] / temperature + stat[1]. Rows that are sure of a token keep the
