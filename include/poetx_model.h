@@ -171,10 +171,10 @@ POETX_API int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const v
  *
  * for scoring, policy training and answers with alternatives; sizes, types,
  * strides and rows as for the loss above (poetx_vocab; `piece` concerns the
- * backward). The temperature and its inverse are positive and finite. The
- * logits are formed tile by tile; with alternatives, those of some tokens at a
- * time are held in the workspace in 16 bits (1 GB, and at least 256 tokens: 512 V
- * bytes, more than 1 GB past V = 2^21).
+ * backward). The temperature is positive and finite, and so is log2(e) / temperature
+ * in float32 (from 4.24e-39 on). The logits are formed tile by tile; with
+ * alternatives, those of some tokens at a time are held in the workspace in 16 bits
+ * (1 GB, and at least 256 tokens: 512 V bytes, more than 1 GB past V = 2^21).
  *  - target [T] int64, or NULL: every token is counted, and there is no logprob
  *    (logprob has to be NULL). A token whose target is outside [0, V) (such as
  *    -100) is not counted: its logprob, entropy and stat are 0, its alternatives

@@ -394,10 +394,11 @@ int poetx_vocab_loss_backward(const poetx_vocab* D, int64_t T, const void* h, in
 // --- log probabilities -----------------------------------------------------------
 
 namespace {
-// factor of the logits, or 0 for a temperature that is refused
+// factor of the logits, or 0 for a temperature that is refused: that of their powers of
+// two is finite, too (0, the maximum's distance, times infinity would be NaN)
 float inverse(float temperature) {
   const float f = 1.f / temperature;
-  return temperature > 0.f && std::isfinite(temperature) && std::isfinite(f) ? f : 0.f;
+  return temperature > 0.f && std::isfinite(temperature) && std::isfinite(f * kLog2e) ? f : 0.f;
 }
 bool top_ok(const poetx_vocab* D, int32_t top) { return top >= 0 && top <= kTopMost && top <= D->V; }
 }  // namespace

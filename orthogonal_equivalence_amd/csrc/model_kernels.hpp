@@ -8,6 +8,8 @@
 
 namespace poetx {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // The norm of x + res (res optional) with y or int8 codes q out; gain null:
 // only the row quantisation of x.
 struct NormFwdDesc {

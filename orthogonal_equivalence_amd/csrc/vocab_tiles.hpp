@@ -7,7 +7,6 @@
 
 namespace poetx {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct TileArgs {
