@@ -697,8 +697,14 @@ __global__ void __launch_bounds__(1024) k_token_join(const TokenArgs a) {
 // Gradient of the logits of a piece in the storage type, in units of the largest
 // gradient and without the factor 1 / temperature, both of which the products'
 // epilogues put back in float32: dl = p (g - b (log p + H)) - g [v = target] with g =
-// -a. log p is kept from passing 0 (a tile of another kind than the forward's sums in
-// another order), and the target's p - 1 is expm1(log p).
+// -a, and the target's p - 1 as expm1(log p).
+//
+// A tile of another kind than the forward's sums in another order, and the largest logit
+// is off the forward's maximum by the rounding of both, 1.5e-5 at 300: more than all of 1
+// - p in a row that is sure of its token. There the distance is known without it: where
+// the other exponentials are under e^0.22 - 1 = 0.25 together, the other logits are at
+// least 1.4 below the maximum, and what is within 0.7 of it is the maximum itself, at a
+// distance of 0. In other rows no logit passes the maximum.
 template <class Cfg>
 __device__ __forceinline__ void token_dlogits_tile(const TokenArgs& a, int m0, int tn, int count, char* smem) {
   const int n0 = tn * Cfg::BN;
@@ -726,9 +732,10 @@ __device__ __forceinline__ void token_dlogits_tile(const TokenArgs& a, int m0, i
         for (int r = 0; r < 4; ++r)
           if (tile_col<Cfg>(wn, lane, j, r) == tcol) target = acc[i][j][r];
     }
+    const float near = st.y < 0.22f ? -0.7f / a.inv_temp : 0.f;
     auto log_p = [&](float l) {
-      const float lp = fmaf(l - st.x, a.inv_temp, -st.y);
-      return lp > 0.f ? 0.f : lp;  // NaN stays
+      const float below = l - st.x;
+      return fmaf(below > near ? 0.f : below, a.inv_temp, -st.y);  // NaN stays
     };
 #pragma unroll
     for (int j = 0; j < Cfg::TN; ++j)
