@@ -41,7 +41,6 @@ struct RowsArgs {
   float scale;
   const float* dent;    // of log probabilities with entropy: the entropies' gradients
   const float* ent_in;  // and the entropies
-  float post;           // factor of both gradients behind the logits
   const uint4* h;  // rows in 16-byte chunks
   int64_t ldh;
   uint4* hc;
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(64 * NW) k_vocab_gather(const RowsArgs a, int 
     *a.r.count = total;
     // with no token counted the sums are empty, and 0 whatever the scale
     if (a.backward)
-      *a.r.unit = (a.dloss || a.dent ? most : total ? a.scale / static_cast<float>(total) : 0.f) * a.post;
+      *a.r.unit = a.dloss || a.dent ? most : total ? a.scale / static_cast<float>(total) : 0.f;
   }
   for (int b = t0; b < t1; b += 64) {
     // every wave numbers the 64 tokens alike; the first writes
@@ -463,7 +462,7 @@ __device__ __forceinline__ void dh_tile(const TileArgs& a, int m0, int tn, int s
     }
     if (a.last && a.splits == 1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] *= unit;
+      for (int i = 0; i < 8; ++i) o[i] = o[i] * unit * a.post;
       tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.r.idx[c]) * a.d + k, o);
     } else {
       tile_store8(sum, o);
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(256) k_vocab_join_splits(const TileArgs a, int
   }
   const float unit = *a.r.unit;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] *= unit;
+  for (int j = 0; j < 8; ++j) o[j] = o[j] * unit * a.post;
   tile_store8(static_cast<T*>(a.out) + (DH ? static_cast<int64_t>(a.r.idx[c]) : a.v0 + c) * a.d + k, o);
 }
 
@@ -568,7 +567,7 @@ __device__ __forceinline__ void dw_tile(const TileArgs& a, int bid, int count, c
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= unit;
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * unit * a.post;
     tile_store8(static_cast<typename Elem<Cfg::ES>::type*>(a.out) + static_cast<int64_t>(a.v0 + m) * a.d + k, o);
   });
 }
@@ -648,7 +647,7 @@ __global__ void __launch_bounds__(CH::NT ? CH::NT : CW::NT, 1) k_vocab_grads(con
 
 void vocab_gather(const VocabDesc& D, bool backward, hipStream_t st) {
   const int es = D.bf16 ? 2 : 4, T = static_cast<int>(D.T);
-  const RowsArgs a{D.target, D.V, T, D.rows, backward, D.lse_in, D.stat_in, D.dloss, D.scale, D.dent, D.ent_in, D.inv_temp,
+  const RowsArgs a{D.target, D.V, T, D.rows, backward, D.lse_in, D.stat_in, D.dloss, D.scale, D.dent, D.ent_in,
                    static_cast<const uint4*>(D.h), D.ldh * es / 16, static_cast<uint4*>(D.hc), D.ldhc * es / 16,
                    static_cast<uint4*>(backward ? D.dh : nullptr), static_cast<int>(D.d * es / 16)};
   // a row a wave; few tokens on as many CUs as they have fours (d = 4096, h not in

@@ -27,6 +27,7 @@ struct TileArgs {
   int splits;      // of K over workgroups
   void* out;
   int tile;        // of the wide ones: dw's, and dh's where it is split
+  float post;      // dh, dw: factor behind the logits (1 / temperature), times the unit maybe past float32
   float beside;    // dh: us of dw's tiles in the same launch, were their K as long as kTileCosts'
 };
 
@@ -212,6 +213,7 @@ inline TileArgs tile_args(const VocabDesc& D) {
   a.r = D.rows;
   a.T = static_cast<int>(D.T);
   a.d = static_cast<int>(D.d);
+  a.post = D.inv_temp;
   return a;
 }
 
