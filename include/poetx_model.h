@@ -231,7 +231,8 @@ POETX_API size_t poetx_token_ws_bytes(const poetx_vocab* D, int64_t T, int op, i
  * empty one's pointer is not used), such as the packed gradients of all layers, the
  * gains' and the vocabulary matrix's. The pointers, sizes and types are host
  * arrays, read before the call returns. Squares and sums are in double, the sum
- * rounded once, to the norm; the factor is formed in double and applied in float32.
+ * rounded once, to the norm; the factor is formed in double and applied in float32, one
+ * below float32's normal numbers in two steps.
  *   norm [1] float on the device.
  *   out[i] may be g[i] itself, which a factor of 1 leaves untouched; apart from
  *       that no output may overlap an input or another output (POETX_EINVAL): a

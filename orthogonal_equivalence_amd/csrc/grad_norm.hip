@@ -153,12 +153,12 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const double* part, int 
 }
 
 template <class T>
-__device__ __forceinline__ void scale_values(const GradEntry& e, int64_t lo, int64_t hi, float f) {
+__device__ __forceinline__ void scale_values(const GradEntry& e, int64_t lo, int64_t hi, float first, float f) {
   const T* g = static_cast<const T*>(e.g);
   T* out = static_cast<T*>(e.out);
   constexpr int es = sizeof(T);
   if ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) store_from_f32(out + i, load_as_f32(g + i) * f);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) store_from_f32(out + i, load_as_f32(g + i) * first * f);
     return;
   }
   walk<true>(g, es, lo, hi,
@@ -167,12 +167,12 @@ __device__ __forceinline__ void scale_values(const GradEntry& e, int64_t lo, int
          uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
          for (int j = 0; j < 4; ++j)
-           x[j] = es == 2 ? pack_bf16x2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xffff0000u) * f)
-                          : __float_as_uint(__uint_as_float(x[j]) * f);
+           x[j] = es == 2 ? pack_bf16x2(__uint_as_float(x[j] << 16) * first * f, __uint_as_float(x[j] & 0xffff0000u) * first * f)
+                          : __float_as_uint(__uint_as_float(x[j]) * first * f);
          const u32x4_t y = {x[0], x[1], x[2], x[3]};
          __builtin_nontemporal_store(y, reinterpret_cast<u32x4_t*>(out + i));
        },
-       [&](int64_t i) { store_from_f32(out + i, load_as_f32(g + i) * f); });
+       [&](int64_t i) { store_from_f32(out + i, load_as_f32(g + i) * first * f); });
 }
 
 // The norm and the scaled values. Each workgroup takes the share that it took of
@@ -184,11 +184,14 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(const GradEntry* table,
   __shared__ double red[kThreads / 64];
   const double size = sqrt(sum_parts(part, gridDim.x, red)), q = max_norm / (size + 1e-6);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(size);
-  const float f = q > 1.0 ? 1.f : static_cast<float>(q);  // NaN stays
+  // a factor below float's normal numbers in two, of which the first takes no bits of values
+  // whose products are normal
+  const float first = q < 0x1p-126 ? 0x1p-126f : 1.f;
+  const float f = q > 1.0 ? 1.f : static_cast<float>(q / first);  // NaN stays
   walk_share<true>(table, count, units, [&](const GradEntry& e, int64_t lo, int64_t hi) {
     if (f == 1.f && e.out == e.g) return;
-    if (e.bf16) scale_values<bf16_t>(e, lo, hi, f);
-    else scale_values<float>(e, lo, hi, f);
+    if (e.bf16) scale_values<bf16_t>(e, lo, hi, first, f);
+    else scale_values<float>(e, lo, hi, first, f);
   });
 }
 
