@@ -505,11 +505,12 @@ __global__ void __launch_bounds__(256) k_vocab_join_splits(const TileArgs a, int
 // workgroups where the tiles of a small vocabulary leave CUs idle.
 //
 // RESID: as in dh, a row of h for each token whose target the row of dw is, in the
-// order of the tokens: every tile looks through the targets for its own (1 to 2% of the
-// backward). Rows with more than kResidMost of them do without: with lists of any length
-// dw was 0.19 to 0.21% off where tokens are as frequent as a tokenizer's, with these 0.20
-// to 0.22, with none 0.24, its own rounding being 0.17, but T = 8192, V = 131072 took 28.1
-// ms in place of 27.1.
+// order of the tokens: every tile of the first split looks through the targets for its own
+// (1 to 2% of the backward at T = 8192; at T = 65536, V = 100 32 of dw's 65 us). Rows with
+// more than kResidMost of them do without: with lists of any length dw was 0.19 to 0.21%
+// off where tokens are as frequent as a tokenizer's, with these 0.20 to 0.22, with none
+// 0.24, its own rounding being 0.17, but T = 8192, V = 131072 took 28.1 ms in place of
+// 27.1.
 constexpr int kResidMost = 16;
 template <class Cfg, bool RESID>
 __device__ __forceinline__ void dw_tile(const TileArgs& a, int bid, int count, char* smem) {
